@@ -244,7 +244,7 @@ def _run_own(st):
         return st["y"]
     if op == "dispatch":
         gq.experts_sort(st["offsets"], st["order"], st["pos"], st["ids"], st["scratch"])
-        gq.experts_gather(st["xs"], st["x"], st["order"])
+        gq.experts_gather(st["xs"], st["x"], st["pos"])
         return {"offsets": st["offsets"], "order": st["order"], "pos": st["pos"], "xs": st["xs"]}
     gq.experts_combine(st["out"], st["y"], st["pos"], st["w"])
     gq.experts_combine_backward(st["dy"], st["dw"], st["dout"], st["y"], st["pos"], st["w"])
