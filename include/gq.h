@@ -30,7 +30,7 @@
  *   - Calls return a gq_status.  GQ_OK is 0; the detail of any other status is
  *     in gq_last_error() (thread-local, valid until the next call on the same
  *     host thread).  On an error the outputs are undefined.
- *   - hessian_* calls are asynchronous: they validate arguments, enqueue kernels
+ *   - hessian_* calls (and the pack products and expert rows below) are asynchronous: they validate arguments, enqueue kernels
  *     and return; they report argument and launch errors only.  psd_project,
  *     gptq_factor, gptq_sweep and gptq_quantize synchronise their stream before
  *     returning, to report data-dependent status (and qerr).
@@ -402,6 +402,128 @@ int rtn_quantize_ex(uint8_t *codes, float *scales, double *qerr_out, const float
 #define GQ_NOALLOC_SCRATCH_BYTES 65536
 int rtn_quantize_noalloc(uint8_t *codes, float *scales, double *qerr_out, const float *W, const float *imp,
                          int64_t N, int64_t K, int64_t group, uint32_t flags, hipStream_t stream);
+
+/*
+ * Products with the packs, the 8-bit pack beside them, and the rows of a mixture
+ * of experts: what runs on a layer once it is packed.  Conventions of this part:
+ *   - activations and outputs are fp32 or bf16 (gq_dtype) rows of a given stride
+ *     in elements (ld*, at least the row's length); packs are contiguous;
+ *   - every call is asynchronous, allocates nothing, reads nothing back and keeps
+ *     nothing, so it can be captured into a HIP graph; only experts_sort takes a
+ *     workspace;
+ *   - outputs must not overlap inputs; the stream belongs to the current device;
+ *   - the same inputs give the same bits: no sum depends on timing;
+ *   - NaN and infinity are not searched for: they spread as in the formula.
+ * An expert's rows are offsets[e] .. offsets[e + 1] - 1 (int32, device, E + 1
+ * entries, as experts_sort writes them) of a matrix of M rows; rows outside
+ * offsets[0] .. offsets[E] - 1 of the output are left as they were.  Entries
+ * outside 0 .. M or out of order are clamped, never followed.
+ */
+#define GQ_MAX_EXPERTS 1024
+
+/*
+ * int4_matmul -- Y = X Wq^T for a weight packed by gptq_sweep, gptq_quantize,
+ * rtn_quantize or their variants:
+ *     Y[m][n] = sum_g scales[n][g] sum_{k in group g} X[m][k] v(codes[n][k]),
+ * v(c) the code, or the NF4 level of c under GQ_NF4 (uniform symmetric int4 with
+ * w ~ code * scale: ork-driver wiki, "Exp 2026-08-18 GPTQ Int4").  Products are
+ * summed in fp32 and rounded once to y_dtype; fp32 X and NF4 levels enter the
+ * bf16 matrix cores as sums of bf16 parts, not rounded to one.
+ *   Y       M x N, y_dtype, written.      X  M x K, x_dtype.
+ *   codes, scales, N, K, group: the pack, as gptq_sweep writes it.
+ *   flags   the flags it was packed with; only GQ_NF4 changes how it is read.
+ * Errors: GQ_ERR_INVALID_ARG, GQ_ERR_HIP (launch).  M == 0 is a no-op.
+ */
+int int4_matmul(void *Y, int y_dtype, int64_t ldy, const void *X, int x_dtype, int64_t ldx, const uint8_t *codes,
+                const float *scales, int64_t M, int64_t N, int64_t K, int64_t group, uint32_t flags,
+                hipStream_t stream);
+
+/* int4_matmul for E experts: codes E x N x K/2 and scales E x N x (K/group), the
+ * rows of expert e times its own pack.  M is the number of rows of X and Y. */
+int int4_matmul_experts(void *Y, int y_dtype, int64_t ldy, const void *X, int x_dtype, int64_t ldx,
+                        const uint8_t *codes, const float *scales, const int32_t *offsets, int64_t E, int64_t M,
+                        int64_t N, int64_t K, int64_t group, uint32_t flags, hipStream_t stream);
+
+/*
+ * fp8_quantize -- round-to-nearest pack to 8-bit floating point (e4m3: 4
+ * exponent and 3 mantissa bits, largest value 448, no infinity), the 8-bit
+ * counterpart of rtn_quantize: one scale = absmax / 448 per block of block_rows
+ * rows x 128 columns, code = e4m3(clamp(x / scale, -448, 448)) with an IEEE fp32
+ * division and ties to even, x ~ code * scale; a block whose scale is 0 takes
+ * codes 0.  The last row and column blocks may be partial.  A block with a NaN
+ * has a NaN scale and NaN codes; one with an infinity an infinite scale, NaN
+ * codes for its infinities and 0 for the rest: either way it dequantises to NaN.
+ *   codes   rows x K bytes.   scales  ceil(rows/block_rows) x ceil(K/128) fp32.
+ *   X       rows x K, x_dtype, stride ldx.    block_rows  1 (activations) or 128
+ *           (weights).
+ * Asynchronous, unlike rtn_quantize: there is no status to report.
+ */
+int fp8_quantize(uint8_t *codes, float *scales, const void *X, int x_dtype, int64_t ldx, int64_t rows, int64_t K,
+                 int64_t block_rows, hipStream_t stream);
+
+/*
+ * fp8_matmul -- Y = X W^T from two e4m3 packs:
+ *     Y[m][n] = sum_b xs[m][b] ws[n / 128][b] sum_{k in block b} Xq[m][k] Wq[n][k],
+ * the inner sums on the fp8 matrix cores, everything summed in fp32 and rounded
+ * once to y_dtype.
+ *   Y  M x N, y_dtype, written.
+ *   Xq, xs  M x K codes, M x ceil(K/128) scales (fp8_quantize, block_rows 1).
+ *   Wq, ws  N x K codes, ceil(N/128) x ceil(K/128) scales (block_rows 128).
+ * Errors as int4_matmul.
+ */
+int fp8_matmul(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, const float *xs, const uint8_t *Wq,
+               const float *ws, int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* fp8_matmul for E experts: Wq E x N x K, ws E x ceil(N/128) x ceil(K/128). */
+int fp8_matmul_experts(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, const float *xs, const uint8_t *Wq,
+                       const float *ws, const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                       hipStream_t stream);
+
+/*
+ * experts_sort -- the n = T k choices of a router ordered by expert, in the order
+ * of the slots within each expert (slot t k + j is token t's j-th choice).  A
+ * choice outside 0 .. E - 1 is dropped: the slot has no row.
+ *   offsets  E + 1 ints: expert e's rows are offsets[e] .. offsets[e + 1] - 1.
+ *   order    n ints: the slot of each row; -1 from offsets[E] on.
+ *   pos      n ints: the row of each slot; -1 for a dropped one.
+ *   ids      n choices of id_bytes (4 or 8) bytes each, signed.
+ *   ws       experts_sort_workspace_size(n, E) bytes.
+ */
+size_t experts_sort_workspace_size(int64_t n, int64_t E);
+int experts_sort(int32_t *offsets, int32_t *order, int32_t *pos, const void *ids, int id_bytes, int64_t n, int64_t E,
+                 void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * experts_gather -- Xs[pos[t][j]] = X[t] for every slot with a row: the
+ * activations in expert order, for each expert's Hessian (hessian_accumulate of
+ * its rows) and product.  Rows that no slot has are left as they were.  Its
+ * gradient is experts_combine without weights.
+ *   Xs  rows x D, stride ldxs.   X  T x D, stride ldx; both of `dtype`.
+ *   pos T x k ints, distinct where not -1; an entry outside 0 .. rows - 1 counts
+ *       as -1.
+ */
+int experts_gather(void *Xs, int64_t ldxs, const void *X, int64_t ldx, int dtype, const int32_t *pos, int64_t rows,
+                   int64_t T, int64_t k, int64_t D, hipStream_t stream);
+
+/*
+ * experts_combine -- out[t] = sum_j weights[t][j] Y[pos[t][j]] over the slots
+ * with a row, added in the order of j in fp32 and rounded once; a token without
+ * rows gets zeros.  weights: T x k fp32, or NULL for all ones (the gradient of
+ * experts_gather).  out T x D and Y rows x D of `dtype`; pos as above.
+ */
+int experts_combine(void *out, int64_t ldo, const void *Y, int64_t ldy, int dtype, const int32_t *pos,
+                    const float *weights, int64_t rows, int64_t T, int64_t k, int64_t D, hipStream_t stream);
+
+/*
+ * experts_combine_backward -- gradient of experts_combine under dout (T x D):
+ *     dY[pos[t][j]] = weights[t][j] dout[t],
+ *     dweights[t][j] = sum_c dout[t][c] Y[pos[t][j]][c]   (0 for a slot without a row).
+ * dY rows x D and dout of `dtype`, dweights T x k fp32; rows of dY that no slot
+ * has are left as they were.
+ */
+int experts_combine_backward(void *dY, int64_t lddy, float *dweights, const void *dout, int64_t ldo, const void *Y,
+                             int64_t ldy, int dtype, const int32_t *pos, const float *weights, int64_t rows,
+                             int64_t T, int64_t k, int64_t D, hipStream_t stream);
 
 /*
  * HFQM calibration package (.calib.hfq), the container that carries stored

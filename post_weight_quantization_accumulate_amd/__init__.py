@@ -25,6 +25,7 @@ GQ_STATIC_GROUPS, GQ_NF4, GQ_ACT_ORDER = 1, 2, 4
 GQ_F32, GQ_BF16 = 0, 1
 GQ_PSD_AUTO, GQ_PSD_F64 = 0, 1
 GQ_SWEEP_AUTO, GQ_SWEEP_F32, GQ_SWEEP_F64 = 0, 1, 2
+GQ_MAX_EXPERTS = 1024
 
 EXPORTS = (
     "gq_abi_version", "gq_last_error", "hessian_accumulate", "hessian_tril_bytes",
@@ -38,6 +39,8 @@ EXPORTS = (
     "hfqm_write", "hfqm_read_header", "hfqm_read_entry", "hfqm_read_payload",
     "hadamard_rotate_rows", "hadamard_rotate_hessian_workspace_size", "hadamard_rotate_hessian",
     "rtn_quantize_noalloc", "hessian_accumulate_chunks_workspace_size", "hessian_accumulate_chunks",
+    "int4_matmul", "int4_matmul_experts", "fp8_quantize", "fp8_matmul", "fp8_matmul_experts",
+    "experts_sort_workspace_size", "experts_sort", "experts_gather", "experts_combine", "experts_combine_backward",
 )
 
 
@@ -102,6 +105,16 @@ def lib() -> ctypes.CDLL:
             "hadamard_rotate_rows": (I, [P, I64, I64, I64, I64, P, P]),
             "hadamard_rotate_hessian_workspace_size": (SZ, [I64]),
             "hadamard_rotate_hessian": (I, [P, I64, I64, P, P, SZ, P]),
+            "int4_matmul": (I, [P, I, I64, P, I, I64, P, P, I64, I64, I64, I64, U32, P]),
+            "int4_matmul_experts": (I, [P, I, I64, P, I, I64, P, P, P, I64, I64, I64, I64, I64, U32, P]),
+            "fp8_quantize": (I, [P, P, P, I, I64, I64, I64, I64, P]),
+            "fp8_matmul": (I, [P, I, I64, P, P, P, P, I64, I64, I64, P]),
+            "fp8_matmul_experts": (I, [P, I, I64, P, P, P, P, P, I64, I64, I64, I64, P]),
+            "experts_sort_workspace_size": (SZ, [I64, I64]),
+            "experts_sort": (I, [P, P, P, P, I, I64, I64, P, SZ, P]),
+            "experts_gather": (I, [P, I64, P, I64, I, P, I64, I64, I64, I64, P]),
+            "experts_combine": (I, [P, I64, P, I64, I, P, P, I64, I64, I64, I64, P]),
+            "experts_combine_backward": (I, [P, I64, P, P, I64, P, I64, I, P, P, I64, I64, I64, I64, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -431,6 +444,205 @@ def hadamard_rotate_hessian(H, block: int, ws, signs=None):
         _need(signs, "signs", torch.float32, K)
     _check(lib().hadamard_rotate_hessian(_ptr(H), K, block, _ptr(signs), _ptr(ws), ws.numel(), _stream(H)),
            "hadamard_rotate_hessian")
+
+
+# ------------------------------------------------------------------ pack products
+_ROW_DTYPES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16}
+
+
+def _rows(t, name, rows=None, cols=None):
+    """(dtype code, row stride) of a 2-D fp32 or bf16 tensor with unit column stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    dt = _ROW_DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be fp32 or bf16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} is {r} x {c}, needs {r if rows is None else rows} x {c if cols is None else cols}")
+    ld = t.stride(0) if r > 1 else c
+    if (c > 1 and t.stride(1) != 1) or ld < c:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return dt, ld
+
+
+def _shape(t, name, dtype, shape):
+    """A contiguous device tensor of this dtype and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(name, first, others, *args):
+    """Call the library on first's device, on that device's current stream."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: every tensor must be on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(status, name)
+
+
+def _group_ok(group, K):
+    if group < 1 or K % group:
+        raise ValueError(f"group {group} does not divide K = {K}")
+
+
+def int4_matmul(Y, X, codes, scales, group: int, flags: int = 0) -> None:
+    """Y = X Wq^T for the int4 (or, with GQ_NF4, NF4) pack of an N x K weight:
+    Y M x N and X M x K fp32 or bf16, codes N x K/2, scales N x K/group."""
+    yd, ldy = _rows(Y, "Y")
+    M, N = Y.shape
+    xd, ldx = _rows(X, "X", M)
+    K = X.shape[1]
+    _group_ok(group, K)
+    _shape(codes, "codes", torch.uint8, (N, K // 2))
+    _shape(scales, "scales", torch.float32, (N, K // group))
+    _launch("int4_matmul", Y, (X, codes, scales), Y.data_ptr(), yd, ldy, X.data_ptr(), xd, ldx, codes.data_ptr(),
+            scales.data_ptr(), M, N, K, group, flags)
+
+
+def int4_matmul_experts(Y, X, codes, scales, offsets, group: int, flags: int = 0) -> None:
+    """int4_matmul of each expert's rows with its pack: codes E x N x K/2, scales
+    E x N x K/group, offsets E + 1 int32 (experts_sort's)."""
+    yd, ldy = _rows(Y, "Y")
+    M, N = Y.shape
+    xd, ldx = _rows(X, "X", M)
+    K, E = X.shape[1], offsets.numel() - 1
+    _group_ok(group, K)
+    _shape(offsets, "offsets", torch.int32, (E + 1,))
+    _shape(codes, "codes", torch.uint8, (E, N, K // 2))
+    _shape(scales, "scales", torch.float32, (E, N, K // group))
+    _launch("int4_matmul_experts", Y, (X, codes, scales, offsets), Y.data_ptr(), yd, ldy, X.data_ptr(), xd, ldx,
+            codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), E, M, N, K, group, flags)
+
+
+def fp8_quantize(codes, scales, X, block_rows: int) -> None:
+    """e4m3 codes of X (rows x K, fp32 or bf16) with one scale absmax/448 per block
+    of block_rows (1 or 128) x 128: codes float8_e4m3fn, scales fp32."""
+    xd, ldx = _rows(X, "X")
+    R, K = X.shape
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    _shape(codes, "codes", torch.float8_e4m3fn, (R, K))
+    _shape(scales, "scales", torch.float32, (-(-R // block_rows), -(-K // 128)))
+    _launch("fp8_quantize", X, (codes, scales), codes.data_ptr(), scales.data_ptr(), X.data_ptr(), xd, ldx, R, K,
+            block_rows)
+
+
+def fp8_matmul(Y, Xq, xs, Wq, ws) -> None:
+    """Y = X W^T (M x N, fp32 or bf16) from fp8_quantize's packs of X (block_rows 1)
+    and W (block_rows 128)."""
+    yd, ldy = _rows(Y, "Y")
+    M, N = Y.shape
+    K = Xq.shape[-1]
+    kb = -(-K // 128)
+    _shape(Xq, "Xq", torch.float8_e4m3fn, (M, K))
+    _shape(xs, "xs", torch.float32, (M, kb))
+    _shape(Wq, "Wq", torch.float8_e4m3fn, (N, K))
+    _shape(ws, "ws", torch.float32, (-(-N // 128), kb))
+    _launch("fp8_matmul", Y, (Xq, xs, Wq, ws), Y.data_ptr(), yd, ldy, Xq.data_ptr(), xs.data_ptr(), Wq.data_ptr(),
+            ws.data_ptr(), M, N, K)
+
+
+def fp8_matmul_experts(Y, Xq, xs, Wq, ws, offsets) -> None:
+    """fp8_matmul of each expert's rows with its pack: Wq E x N x K, ws
+    E x ceil(N/128) x ceil(K/128), offsets E + 1 int32 (experts_sort's)."""
+    yd, ldy = _rows(Y, "Y")
+    M, N = Y.shape
+    K, E = Xq.shape[-1], offsets.numel() - 1
+    kb = -(-K // 128)
+    _shape(offsets, "offsets", torch.int32, (E + 1,))
+    _shape(Xq, "Xq", torch.float8_e4m3fn, (M, K))
+    _shape(xs, "xs", torch.float32, (M, kb))
+    _shape(Wq, "Wq", torch.float8_e4m3fn, (E, N, K))
+    _shape(ws, "ws", torch.float32, (E, -(-N // 128), kb))
+    _launch("fp8_matmul_experts", Y, (Xq, xs, Wq, ws, offsets), Y.data_ptr(), yd, ldy, Xq.data_ptr(), xs.data_ptr(),
+            Wq.data_ptr(), ws.data_ptr(), offsets.data_ptr(), E, M, N, K)
+
+
+# ------------------------------------------------------------------ rows of experts
+def experts_sort_workspace_size(n: int, E: int) -> int:
+    return int(lib().experts_sort_workspace_size(n, E))
+
+
+def experts_sort(offsets, order, pos, ids, ws) -> None:
+    """A router's choices (ids: T x k, int32 or int64) ordered by expert, E =
+    offsets.numel() - 1 experts: offsets (E + 1), order (T k, each row's slot) and
+    pos (like ids, each slot's row or -1), all int32."""
+    n, E = ids.numel(), offsets.numel() - 1
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64")
+    _shape(ids, "ids", ids.dtype, tuple(ids.shape))
+    _shape(offsets, "offsets", torch.int32, (E + 1,))
+    _shape(order, "order", torch.int32, (n,))
+    _shape(pos, "pos", torch.int32, tuple(ids.shape))
+    _shape(ws, "ws", torch.uint8, (ws.numel(),))
+    _launch("experts_sort", ids, (offsets, order, pos, ws), offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
+            ids.data_ptr(), ids.element_size(), n, E, ws.data_ptr(), ws.numel())
+
+
+def _pos(pos, T):
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or pos.shape[0] != T:
+        raise ValueError("pos must be T x k")
+    _shape(pos, "pos", torch.int32, tuple(pos.shape))
+    return pos.shape[1]
+
+
+def experts_gather(Xs, X, pos) -> None:
+    """Xs[pos[t, j]] = X[t] for every slot with a row (pos from experts_sort)."""
+    dt, ldx = _rows(X, "X")
+    T, D = X.shape
+    dts, ldxs = _rows(Xs, "Xs", None, D)
+    if dts != dt:
+        raise ValueError("Xs and X must have one dtype")
+    k = _pos(pos, T)
+    _launch("experts_gather", X, (Xs, pos), Xs.data_ptr(), ldxs, X.data_ptr(), ldx, dt, pos.data_ptr(), Xs.shape[0],
+            T, k, D)
+
+
+def experts_combine(out, Y, pos, weights=None) -> None:
+    """out[t] = sum_j weights[t, j] Y[pos[t, j]] over the slots with a row (weights
+    T x k fp32, or None for ones: the gradient of experts_gather)."""
+    dt, ldo = _rows(out, "out")
+    T, D = out.shape
+    dty, ldy = _rows(Y, "Y", None, D)
+    if dty != dt:
+        raise ValueError("out and Y must have one dtype")
+    k = _pos(pos, T)
+    if weights is not None:
+        _shape(weights, "weights", torch.float32, (T, k))
+    _launch("experts_combine", out, (Y, pos, weights), out.data_ptr(), ldo, Y.data_ptr(), ldy, dt, pos.data_ptr(),
+            None if weights is None else weights.data_ptr(), Y.shape[0], T, k, D)
+
+
+def experts_combine_backward(dY, dweights, dout, Y, pos, weights) -> None:
+    """Gradient of experts_combine under dout: dY[pos[t, j]] = weights[t, j] dout[t],
+    dweights[t, j] = <dout[t], Y[pos[t, j]]>."""
+    dt, ldo = _rows(dout, "dout")
+    T, D = dout.shape
+    rows = Y.shape[0]
+    dty, ldy = _rows(Y, "Y", None, D)
+    dtd, lddy = _rows(dY, "dY", rows, D)
+    if dty != dt or dtd != dt:
+        raise ValueError("dY, dout and Y must have one dtype")
+    k = _pos(pos, T)
+    _shape(weights, "weights", torch.float32, (T, k))
+    _shape(dweights, "dweights", torch.float32, (T, k))
+    _launch("experts_combine_backward", dout, (dY, dweights, Y, pos, weights), dY.data_ptr(), lddy,
+            dweights.data_ptr(), dout.data_ptr(), ldo, Y.data_ptr(), ldy, dt, pos.data_ptr(), weights.data_ptr(), rows,
+            T, k, D)
 
 
 # ------------------------------------------------------------------ HFQM package

@@ -1,0 +1,221 @@
+// fp8.hip -- 8-bit floating point (e4m3) packs with one scale per block of 128
+// columns, and products of two of them.
+#include "gq.h"
+#include "gq_internal.h"
+#include "matmul.h"
+
+namespace gq {
+namespace {
+
+constexpr int kBlock = 128;
+constexpr float kE4m3Max = 448.0f;
+
+__device__ inline float load_f(const float *p) { return *p; }
+__device__ inline float load_f(const __bf16 *p) { return (float)*p; }
+
+// The code of x under scale s: e4m3 of x / s (IEEE division, round to nearest
+// even, clamped to +-448, NaN kept); 0 where the scale is 0.
+__device__ inline unsigned fp8_code2(float x0, float x1, float s)
+{
+    float q0 = x0 / s, q1 = x1 / s;
+    q0 = q0 != q0 ? q0 : fminf(fmaxf(q0, -kE4m3Max), kE4m3Max);
+    q1 = q1 != q1 ? q1 : fminf(fmaxf(q1, -kE4m3Max), kE4m3Max);
+    return s == 0.0f ? 0u : (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(q0, q1, 0, false) & 0xFFFFu;
+}
+
+// One block of BR x 128 elements per workgroup: its largest magnitude (as bits,
+// so that a NaN is the largest of all), the scale, the codes.
+template <typename TX, int BR>
+__global__ __launch_bounds__(256) void fp8_pack_kernel(uint8_t *codes, float *scales, const TX *X, int64_t ldx,
+                                                       int64_t rows, int64_t K, int64_t kb)
+{
+    __shared__ unsigned red[4];
+    const int64_t rb = grid_row(), cb = blockIdx.x;
+    if (rb * BR >= rows) return;
+    const int tid = threadIdx.x;
+    unsigned mx = 0;
+    for (int i = tid; i < BR * kBlock; i += 256) {
+        const int64_t r = rb * BR + i / kBlock, c = cb * kBlock + i % kBlock;
+        if (r < rows && c < K) mx = max(mx, __float_as_uint(load_f(X + r * ldx + c)) & 0x7FFFFFFFu);
+    }
+    for (int d = 32; d; d >>= 1) mx = max(mx, (unsigned)__shfl_xor((int)mx, d));
+    if ((tid & 63) == 0) red[tid >> 6] = mx;
+    __syncthreads();
+    mx = max(max(red[0], red[1]), max(red[2], red[3]));
+    const float s = __uint_as_float(mx) / kE4m3Max;
+    if (tid == 0) scales[rb * kb + cb] = s;
+    for (int i = tid; i < BR * kBlock; i += 256) {
+        const int64_t r = rb * BR + i / kBlock, c = cb * kBlock + i % kBlock;
+        if (r < rows && c < K) codes[r * K + c] = (uint8_t)fp8_code2(load_f(X + r * ldx + c), 0.0f, s);
+    }
+}
+
+template <typename TX>
+hipError_t launch_pack(uint8_t *codes, float *scales, const TX *X, int64_t ldx, int64_t rows, int64_t K,
+                       int64_t block_rows, hipStream_t s)
+{
+    const int64_t kb = (K + kBlock - 1) / kBlock;
+    const dim3 grid = tile_grid(kb, (rows + block_rows - 1) / block_rows);
+    if (block_rows == 1)
+        hipLaunchKernelGGL((fp8_pack_kernel<TX, 1>), grid, dim3(256), 0, s, codes, scales, X, ldx, rows, K, kb);
+    else
+        hipLaunchKernelGGL((fp8_pack_kernel<TX, 128>), grid, dim3(256), 0, s, codes, scales, X, ldx, rows, K, kb);
+    return hipGetLastError();
+}
+
+struct F8Args {
+    void *Y;
+    const uint8_t *Xq, *Wq;
+    const float *xs, *ws;
+    const int *offsets;
+    int64_t M, ldy, E;
+    int N, K, kb;
+};
+
+// Four e4m3 codes as bf16, exactly (3 mantissa bits, exponents -9 .. 8).
+__device__ inline void bf16_of_fp8(unsigned w, bf16x2 &lo, bf16x2 &hi)
+{
+    lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
+}
+__device__ inline bf16x8 bf16_of_fp8(unsigned w0, unsigned w1)
+{
+    bf16x2 a, b, c, d;
+    bf16_of_fp8(w0, a, b);
+    bf16_of_fp8(w1, c, d);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Codes k .. k + 7 of a row as bf16, zero past K.
+template <bool VEC> __device__ inline bf16x8 load_f8(const uint8_t *row, int k, int K)
+{
+    unsigned w[2] = {0, 0};
+    if constexpr (VEC) {
+        if (k < K) {
+            const uint2 v = *(const uint2 *)(row + k);
+            w[0] = v.x;
+            w[1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (k + t < K) w[t / 4] |= (unsigned)row[k + t] << (8 * (t & 3));
+    }
+    return bf16_of_fp8(w[0], w[1]);
+}
+
+constexpr int kWaves = 4;
+
+// The fp8 matrix instructions add the 8 products of a lane's 8 consecutive k with
+// all but about 14 bits of the largest one cut off, and only the sums of 8 in
+// fp32 (seen by probing with powers of two); e4m3 codes fit bf16 exactly, and the
+// bf16 instructions keep fp32 throughout at half the rate.
+//
+// One 16 x 16 tile of Y per workgroup, its blocks of 128 k dealt to four waves
+// and their sums added through LDS in wave order.
+template <typename TY, bool VEC> __global__ __launch_bounds__(64 * kWaves) void fp8_direct_kernel(F8Args a)
+{
+    __shared__ float red[kWaves][256];
+    RowTile rt;
+    if (!row_tile(a.offsets, (int)a.E, a.M, 16, grid_row(), rt)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, q = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const int n = min(n0 + r, a.N - 1);
+    const int64_t m = min(rt.r0 + r, rt.r1 - 1);
+    const uint8_t *x = a.Xq + m * a.K;
+    const uint8_t *w = a.Wq + (rt.e * a.N + n) * (int64_t)a.K;
+    const float *sx = a.xs + m * a.kb;
+    const float *sw = a.ws + (rt.e * ((a.N + kBlock - 1) / kBlock) + n0 / kBlock) * (int64_t)a.kb;
+    f32x4 acc{};
+    for (int b = wave; b < a.kb; b += kWaves) {
+        f32x4 part{};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = b * kBlock + 32 * j + 8 * q;
+            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(load_f8<VEC>(w, k, a.K), load_f8<VEC>(x, k, a.K), part,
+                                                           0, 0, 0);
+        }
+        const float s = sx[b] * sw[b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, part[i], acc[i]);
+    }
+    // acc[i]: column n0 + 4 q + i of row r
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][16 * r + 4 * q + i] = acc[i];
+    __syncthreads();
+    const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
+    float v = red[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) v += red[i][threadIdx.x];
+    if (rt.r0 + row < rt.r1 && n0 + col < a.N) store_y((TY *)a.Y + (rt.r0 + row) * a.ldy + n0 + col, v);
+}
+
+template <typename TY> hipError_t launch_fp8(F8Args a, hipStream_t s)
+{
+    const dim3 grid = tile_grid((a.N + 15) / 16, row_tiles(a.offsets != nullptr, a.E, a.M, 16));
+    const bool vec = a.K % 8 == 0 && ((uintptr_t)a.Xq & 7) == 0 && ((uintptr_t)a.Wq & 7) == 0;
+    if (vec) hipLaunchKernelGGL((fp8_direct_kernel<TY, true>), grid, dim3(64 * kWaves), 0, s, a);
+    else hipLaunchKernelGGL((fp8_direct_kernel<TY, false>), grid, dim3(64 * kWaves), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace gq
+
+using namespace gq;
+
+namespace {
+
+int fp8_run(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, const float *xs, const uint8_t *Wq, const float *ws,
+            const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K, hipStream_t stream)
+{
+    if (y_dtype != GQ_F32 && y_dtype != GQ_BF16) return set_error(GQ_ERR_INVALID_ARG, "unknown dtype");
+    if (M < 0 || N < 1 || K < 1) return set_error(GQ_ERR_INVALID_ARG, "M must be >= 0, N and K >= 1");
+    if (ldy < N) return set_error(GQ_ERR_INVALID_ARG, "a row stride is below the row's length");
+    if (M > INT32_MAX || N > (1 << 24) || K > (1 << 24)) return set_error(GQ_ERR_INVALID_ARG, "size too large");
+    if (M == 0) return set_error(GQ_OK, "");
+    if (!Y || !Xq || !xs || !Wq || !ws) return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
+    F8Args a{};
+    a.Y = Y; a.Xq = Xq; a.Wq = Wq; a.xs = xs; a.ws = ws; a.offsets = offsets;
+    a.M = M; a.ldy = ldy; a.E = E;
+    a.N = (int)N; a.K = (int)K; a.kb = (int)((K + kBlock - 1) / kBlock);
+    const hipError_t e = y_dtype == GQ_F32 ? launch_fp8<float>(a, stream) : launch_fp8<__bf16>(a, stream);
+    return e == hipSuccess ? set_error(GQ_OK, "") : set_error(GQ_ERR_HIP, hipGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_quantize(uint8_t *codes, float *scales, const void *X, int x_dtype, int64_t ldx, int64_t rows, int64_t K,
+                 int64_t block_rows, hipStream_t stream)
+{
+    if (x_dtype != GQ_F32 && x_dtype != GQ_BF16) return set_error(GQ_ERR_INVALID_ARG, "unknown dtype");
+    if (block_rows != 1 && block_rows != 128) return set_error(GQ_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+    if (rows < 0 || K < 1 || ldx < K) return set_error(GQ_ERR_INVALID_ARG, "bad sizes");
+    if (rows == 0) return set_error(GQ_OK, "");
+    if (!codes || !scales || !X) return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
+    if (K > (1 << 24) || rows > INT32_MAX) return set_error(GQ_ERR_INVALID_ARG, "size too large");
+    const hipError_t e = x_dtype == GQ_F32
+                             ? launch_pack(codes, scales, (const float *)X, ldx, rows, K, block_rows, stream)
+                             : launch_pack(codes, scales, (const __bf16 *)X, ldx, rows, K, block_rows, stream);
+    return e == hipSuccess ? set_error(GQ_OK, "") : set_error(GQ_ERR_HIP, hipGetErrorString(e));
+}
+
+int fp8_matmul(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, const float *xs, const uint8_t *Wq,
+               const float *ws, int64_t M, int64_t N, int64_t K, hipStream_t stream)
+{
+    return fp8_run(Y, y_dtype, ldy, Xq, xs, Wq, ws, nullptr, 1, M, N, K, stream);
+}
+
+int fp8_matmul_experts(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, const float *xs, const uint8_t *Wq,
+                       const float *ws, const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                       hipStream_t stream)
+{
+    if (E < 1 || E > GQ_MAX_EXPERTS) return set_error(GQ_ERR_INVALID_ARG, "E must be 1 .. GQ_MAX_EXPERTS");
+    if (!offsets) return set_error(GQ_ERR_INVALID_ARG, "null offsets");
+    return fp8_run(Y, y_dtype, ldy, Xq, xs, Wq, ws, offsets, E, M, N, K, stream);
+}
+
+}  // extern "C"

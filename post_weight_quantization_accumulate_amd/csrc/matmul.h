@@ -1,0 +1,108 @@
+// matmul.h -- shared parts of the pack products (int4mm.hip, fp8.hip): the row
+// tile of a workgroup with and without experts, bf16 parts of fp32 values, and
+// rounding to the output type.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gq {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+// Rows r0 .. r1 - 1 of X and Y that a workgroup takes, and the pack they go with.
+struct RowTile {
+    int64_t r0, r1;
+    int64_t e;
+};
+
+// Row tile number `t` of tiles of TM rows.  Without offsets the rows are
+// 0 .. M - 1 of pack 0.  With offsets (E + 1 device ints) expert e has the rows
+// offsets[e] .. offsets[e + 1] - 1, in tiles of its own.  The tiles are counted
+// 64 experts at a time, one per lane, with a wave prefix sum, so no host copy of
+// the offsets is needed; every wave of a workgroup finds the same answer by
+// itself.  The offsets are clamped to 0 <= offsets[e] <= offsets[e + 1] <= M, so
+// that no value of theirs leads outside X and Y.  False: no such tile.
+__device__ inline bool row_tile(const int *offsets, int E, int64_t M, int TM, int64_t t, RowTile &out)
+{
+    if (!offsets) {
+        out.r0 = t * TM;
+        out.r1 = min(out.r0 + TM, M);
+        out.e = 0;
+        return out.r0 < M;
+    }
+    const int lane = threadIdx.x & 63;
+    int want = (int)t;
+    for (int base = 0; base < E; base += 64) {
+        int lo = 0, hi = 0;
+        if (base + lane < E) {
+            lo = min(max(offsets[base + lane], 0), (int)M);
+            hi = min(max(offsets[base + lane + 1], lo), (int)M);
+        }
+        const int nt = (hi - lo) / TM + ((hi - lo) % TM != 0);
+        int inc = nt;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(inc, d);
+            if (lane >= d) inc += v;
+        }
+        const int total = __shfl(inc, 63);
+        if (want < total) {
+            const int f = __builtin_ctzll(__ballot(inc > want));
+            const int first = __shfl(inc - nt, f);
+            const int elo = __shfl(lo, f), ehi = __shfl(hi, f);
+            out.r0 = elo + (int64_t)(want - first) * TM;
+            out.r1 = min(out.r0 + TM, (int64_t)ehi);
+            out.e = base + f;
+            return true;
+        }
+        want -= total;
+    }
+    return false;
+}
+
+// An upper bound of the number of row tiles: with experts every tile holds a
+// row and every expert adds at most one partly filled tile.
+inline int64_t row_tiles(bool experts, int64_t E, int64_t M, int64_t TM)
+{
+    if (!experts) return (M + TM - 1) / TM;
+    const int64_t n = M / TM + E;
+    return n < M ? n : M;
+}
+
+// A grid of nt column tiles (x) by mt row tiles (y and z): row tile
+// blockIdx.z * kGridRows + blockIdx.y.
+constexpr int64_t kGridRows = 32768;
+inline dim3 tile_grid(int64_t nt, int64_t mt)
+{
+    const int64_t z = (mt + kGridRows - 1) / kGridRows;
+    return dim3((unsigned)nt, (unsigned)(z > 1 ? kGridRows : mt), (unsigned)z);
+}
+__device__ inline int64_t grid_row() { return (int64_t)blockIdx.z * kGridRows + blockIdx.y; }
+
+// fp32 as a sum of three bf16 values, 8 leading bits each, by truncation: the
+// sum is exact for every finite value whose last part is not below bf16's
+// smallest (2^-133).  Infinity and NaN go into the first part alone, so that
+// they meet the other operand as they would unsplit.
+__device__ inline void split3(float v, unsigned short &h, unsigned short &m, unsigned short &l)
+{
+    const unsigned b = __float_as_uint(v);
+    const bool special = (b & 0x7F800000u) == 0x7F800000u;
+    unsigned hb = b & 0xFFFF0000u;
+    if (special && (b & 0x007FFFFFu)) hb |= 0x00400000u;     // a NaN stays one
+    const float r = special ? 0.0f : v - __uint_as_float(hb);
+    const unsigned mb = __float_as_uint(r) & 0xFFFF0000u;
+    const float q = r - __uint_as_float(mb);
+    h = (unsigned short)(hb >> 16);
+    m = (unsigned short)(mb >> 16);
+    l = (unsigned short)(__float_as_uint(q) >> 16);
+}
+
+__device__ inline void store_y(float *p, float v) { *p = v; }
+__device__ inline void store_y(__bf16 *p, float v) { *p = (__bf16)v; }
+
+}  // namespace gq

@@ -1,0 +1,303 @@
+"""GPU parity of the expert rows (experts_sort, experts_gather, experts_combine and
+its gradient) with a plain 64-bit form, and of a packed mixture layer end to end.
+
+Tolerances: places are whole numbers and copies bit for bit; a sum of n products
+in fp32 is off by at most (n + 1) 2^-24 of the sum of their magnitudes, an output
+in bf16 by half a step (2^-8 relative) more."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def gq():
+    import post_weight_quantization_accumulate_amd as m
+    assert torch.cuda.is_available()
+    m.lib()
+    return m
+
+
+def _sort(gq, ids, E):
+    n = ids.numel()
+    off = torch.full((E + 1,), -9, dtype=torch.int32, device=DEV)
+    order = torch.full((n,), -9, dtype=torch.int32, device=DEV)
+    pos = torch.full(tuple(ids.shape), -9, dtype=torch.int32, device=DEV)
+    gq.experts_sort(off, order, pos, ids.to(DEV), gq.workspace(gq.experts_sort_workspace_size(n, E), DEV))
+    return off, order, pos
+
+
+def _sort_ref(ids, E):
+    ids = ids.reshape(-1).numpy()
+    live = np.flatnonzero((ids >= 0) & (ids < E))
+    rows = live[np.argsort(ids[live], kind="stable")]
+    order = np.full(ids.size, -1, np.int32)
+    order[:rows.size] = rows
+    pos = np.full(ids.size, -1, np.int32)
+    pos[rows] = np.arange(rows.size)
+    off = np.concatenate([[0], np.cumsum(np.bincount(ids[live], minlength=E))]).astype(np.int32)
+    return off, order, pos
+
+
+@pytest.mark.parametrize("dt", [torch.int32, torch.int64])
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (4, 8, 128), (7, 3, 5), (1000, 2, 64), (512, 2, 8), (128, 8, 1024),
+                                   (1025, 1, 3), (5000, 8, 128), (0, 2, 4), (300, 7, 1023), (3000, 4, 2), (40000, 3, 60),
+                                   (129, 8, 16), (2047, 1, 256)])
+def test_sort(gq, T, k, E, dt):
+    rng = np.random.default_rng(T + k + E)
+    ids = torch.from_numpy(rng.integers(-1, E + 1, (T, k))).to(dt)       # some of them dropped, on both sides
+    got = _sort(gq, ids, E)
+    for a, b in zip(got, _sort_ref(ids, E)):
+        assert np.array_equal(a.cpu().numpy().reshape(-1), b)
+
+
+@pytest.mark.parametrize("fill", [-1, 0, 5, 7])
+def test_sort_one_expert_takes_all(gq, fill):
+    ids = torch.full((900, 3), fill, dtype=torch.int32)
+    for a, b in zip(_sort(gq, ids, 7), _sort_ref(ids, 7)):
+        assert np.array_equal(a.cpu().numpy().reshape(-1), b)
+
+
+def test_sort_ids_past_32_bits_are_dropped(gq):
+    ids = torch.tensor([[1 << 32, 1], [-(1 << 32), (1 << 40) + 2], [0, 2]])
+    off, order, pos = _sort(gq, ids, 3)
+    assert pos.cpu().tolist() == [[-1, 1], [-1, -1], [0, 2]] and off.cpu().tolist() == [0, 1, 2, 3]
+
+
+def _routing(rng, T, k, E):
+    ids = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    ids[rng.random((T, k)) < 0.15] = -1
+    if T > 2:
+        ids[T // 2] = -1                              # a token that nobody takes
+    return torch.from_numpy(ids)
+
+
+SHAPES = [(1, 1, 1, 4, 0), (5, 2, 4, 1001, 0), (33, 8, 16, 64, 3), (40, 3, 9, 5120, 0), (17, 4, 8, 2056, 8), (3, 6, 6, 7, 1),
+          (300, 2, 3, 520, 0), (9, 40, 50, 96, 0)]
+
+
+@pytest.mark.parametrize("xd", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,k,E,D,pad", SHAPES)
+def test_gather_and_combine(gq, T, k, E, D, pad, xd):
+    rng = np.random.default_rng(T * D)
+    ids = _routing(rng, T, k, E)
+    off, _, pos = _sort(gq, ids, E)
+    kept = int(off[-1])
+    x = torch.from_numpy(rng.standard_normal((T, D + pad)).astype(np.float32)).to(DT[xd]).to(DEV)
+    xs = torch.full((T * k, D + pad), 7.0, dtype=DT[xd], device=DEV)
+    gq.experts_gather(xs[:, :D], x[:, :D], pos)
+    p = pos.cpu().numpy()
+    want = np.full((T * k, D), 7.0)
+    for t in range(T):
+        for j in range(k):
+            if p[t, j] >= 0:
+                want[p[t, j]] = x[t, :D].double().cpu().numpy()
+    assert np.array_equal(xs[:, :D].double().cpu().numpy(), want)
+    assert (xs[:, D:] == 7.0).all() and (xs[kept:] == 7.0).all()
+
+    y = torch.from_numpy(rng.standard_normal((T * k, D + pad)).astype(np.float32)).to(DT[xd]).to(DEV)
+    y[kept:] = float("nan")                            # rows of nobody are not read
+    w = torch.from_numpy(rng.random((T, k)).astype(np.float32)).to(DEV)
+    w[pos < 0] = float("nan")                          # nor are the weights of dropped slots
+    y64 = y[:, :D].double().cpu().numpy()
+    for weights in (w, None):
+        out = torch.full((T, D + pad), 7.0, dtype=DT[xd], device=DEV)
+        gq.experts_combine(out[:, :D], y[:, :D], pos, weights)
+        ref, mag = np.zeros((T, D)), np.zeros((T, D))
+        for t in range(T):
+            for j in range(k):
+                if p[t, j] >= 0:
+                    term = (1.0 if weights is None else float(w[t, j])) * y64[p[t, j]]
+                    ref[t] += term
+                    mag[t] += np.abs(term)
+        got = out[:, :D].double().cpu().numpy()
+        assert (np.abs(got - ref) <= (k + 1) * 2.0 ** -24 * mag * (1 + HALF[xd]) + HALF[xd] * np.abs(ref)).all()
+        assert (out[:, D:] == 7.0).all()
+
+
+@pytest.mark.parametrize("xd", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,k,E,D,pad", SHAPES)
+def test_combine_backward(gq, T, k, E, D, pad, xd):
+    rng = np.random.default_rng(T + D)
+    _, _, pos = _sort(gq, _routing(rng, T, k, E), E)
+    p = pos.cpu().numpy()
+    kept = int((p >= 0).sum())
+    mk = lambda r: torch.from_numpy(rng.standard_normal((r, D + pad)).astype(np.float32)).to(DT[xd]).to(DEV)   # noqa: E731
+    y, g = mk(T * k), mk(T)
+    y[kept:] = float("nan")
+    w = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).to(DEV)
+    dy = torch.full((T * k, D + pad), 7.0, dtype=DT[xd], device=DEV)
+    dw = torch.full((T, k), 7.0, device=DEV)
+    gq.experts_combine_backward(dy[:, :D], dw, g[:, :D], y[:, :D], pos, w)
+    g64, y64, w64 = (a.double().cpu().numpy() for a in (g[:, :D], y[:, :D], w))
+    got_dy, got_dw = dy[:, :D].double().cpu().numpy(), dw.double().cpu().numpy()
+    for t in range(T):
+        for j in range(k):
+            if p[t, j] < 0:
+                assert got_dw[t, j] == 0.0
+                continue
+            ref = w64[t, j] * g64[t]
+            assert (np.abs(got_dy[p[t, j]] - ref) <= (HALF[xd] + 2.0 ** -24) * np.abs(ref)).all()
+            prod = g64[t] * y64[p[t, j]]
+            assert abs(got_dw[t, j] - prod.sum()) <= (D + 1) * 2.0 ** -24 * np.abs(prod).sum()
+    assert (dy[kept:] == 7.0).all() and (dy[:, D:] == 7.0).all()
+
+
+def test_gradient_against_differences(gq):
+    """L = <dout, combine(Y, w)> is linear in w and in Y: a step of any size gives the
+    gradient up to the rounding of L, (D + k + 2) 2^-24 of its terms' magnitudes each time."""
+    rng = np.random.default_rng(11)
+    T, k, E, D = 6, 3, 5, 40
+    _, _, pos = _sort(gq, _routing(rng, T, k, E), E)
+    y, g, w = (torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(DEV) for s in [(T * k, D), (T, D), (T, k)])
+
+    def loss(y, w):
+        out = torch.empty(T, D, device=DEV)
+        gq.experts_combine(out, y, pos, w)
+        return float((out.double() * g.double()).sum())
+
+    dy, dw = torch.zeros(T * k, D, device=DEV), torch.zeros(T, k, device=DEV)
+    gq.experts_combine_backward(dy, dw, g, y, pos, w)
+    base = loss(y, w)
+    tol = (D + k + 2) * 2.0 ** -24 * 4 * float((w.abs().max() + 1) * y.abs().max() * g.abs().sum() * k)
+    for t, j in [(0, 0), (2, 1), (5, 2), (3, 0)]:
+        w1 = w.clone()
+        w1[t, j] += 1.0
+        assert abs(loss(y, w1) - base - float(dw[t, j])) <= tol
+        r = int(pos[t, j])
+        if r >= 0:
+            y1 = y.clone()
+            y1[r, 7] += 1.0
+            assert abs(loss(y1, w) - base - float(dy[r, 7])) <= tol
+
+
+def test_gather_gradient_is_the_unweighted_combine(gq):
+    rng = np.random.default_rng(12)
+    T, k, E, D = 20, 4, 6, 72
+    _, _, pos = _sort(gq, _routing(rng, T, k, E), E)
+    dxs = torch.from_numpy(rng.standard_normal((T * k, D)).astype(np.float32)).to(DEV)
+    dx = torch.empty(T, D, device=DEV)
+    gq.experts_combine(dx, dxs, pos)
+    x = torch.zeros(T, D, dtype=torch.float64, requires_grad=True)
+    p = pos.cpu().long()
+    xs = torch.zeros(T * k, D, dtype=torch.float64)
+    xs = xs.index_put((p[p >= 0],), x.unsqueeze(1).expand(T, k, D)[p >= 0])
+    (xs * dxs.double().cpu()).sum().backward()
+    assert (dx.double().cpu() - x.grad).abs().max() <= (k + 1) * 2.0 ** -24 * k * float(dxs.abs().max())
+
+
+def test_positions_outside_the_rows_count_as_dropped(gq):
+    T, k, D, rows = 3, 2, 24, 4
+    pos = torch.tensor([[0, 4], [1 << 30, 2], [-7, 3]], dtype=torch.int32, device=DEV)
+    x = torch.arange(T * D, dtype=torch.float32, device=DEV).view(T, D)
+    xs = torch.full((rows + 1, D), 7.0, device=DEV)
+    gq.experts_gather(xs[:rows], x, pos)
+    assert torch.equal(xs[0], x[0]) and torch.equal(xs[2], x[1]) and torch.equal(xs[3], x[2])
+    assert (xs[1] == 7.0).all() and (xs[rows] == 7.0).all()
+    out = torch.empty(T, D, device=DEV)
+    gq.experts_combine(out, xs[:rows], pos)
+    assert torch.equal(out, x)
+    dy, dw = torch.full((rows + 1, D), 7.0, device=DEV), torch.empty(T, k, device=DEV)
+    gq.experts_combine_backward(dy[:rows], dw, x, xs[:rows], pos, torch.ones(T, k, device=DEV))
+    assert torch.equal(dy[0], x[0]) and (dy[1] == 7.0).all() and (dy[rows] == 7.0).all()
+    assert dw[0, 1] == 0 and dw[1, 0] == 0 and dw[2, 0] == 0
+
+
+def test_experts_in_a_graph(gq):
+    rng = np.random.default_rng(13)
+    T, k, E, D = 70, 4, 16, 136
+    ids = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    x, w = torch.zeros(T, D, device=DEV), torch.zeros(T, k, device=DEV)
+    off, order = torch.zeros(E + 1, dtype=torch.int32, device=DEV), torch.zeros(T * k, dtype=torch.int32, device=DEV)
+    pos, ws = torch.zeros(T, k, dtype=torch.int32, device=DEV), gq.workspace(gq.experts_sort_workspace_size(T * k, E), DEV)
+    xs, out = torch.zeros(T * k, D, device=DEV), torch.zeros(T, D, device=DEV)
+    dy, dw = torch.zeros(T * k, D, device=DEV), torch.zeros(T, k, device=DEV)
+    outs = (off, order, pos, xs, out, dy, dw)
+
+    def calls():
+        gq.experts_sort(off, order, pos, ids, ws)
+        gq.experts_gather(xs, x, pos)
+        gq.experts_combine(out, xs, pos, w)
+        gq.experts_combine_backward(dy, dw, x, xs, pos, w)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        calls()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for i in range(4):
+        ids.copy_(_routing(rng, T, k, E))
+        x.copy_(torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)))
+        w.copy_(torch.from_numpy(rng.random((T, k)).astype(np.float32)))
+        for o in outs:
+            o.zero_()
+        calls()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), i
+
+
+def test_packed_mixture_layer(gq):
+    """The whole run on a small mixture layer: rows by expert, each expert's Hessian from its own
+    rows, GPTQ int4 packs and 8-bit packs, their products over the sorted rows, the rows back with
+    the router's weights, and the gradient.  Every stage against 64 bits on the stage's own inputs."""
+    rng = np.random.default_rng(14)
+    T, k, E, K, N, G = 600, 2, 4, 256, 192, 128
+    ids = _routing(rng, T, k, E)
+    off, order, pos = _sort(gq, ids, E)
+    edge = off.cpu().tolist()
+    kept = edge[-1]
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    xs = torch.zeros(T * k, K, dtype=torch.bfloat16, device=DEV)
+    gq.experts_gather(xs, x, pos)
+    W = torch.from_numpy(rng.standard_normal((E, N, K)).astype(np.float32) * 0.02).to(DEV)
+    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(E, N, K // G, device=DEV)
+    wq = torch.empty(E, N, K, dtype=torch.float8_e4m3fn, device=DEV)
+    ws = torch.empty(E, -(-N // 128), K // 128, device=DEV)
+    for e in range(E):
+        H = torch.zeros(K, K, device=DEV)
+        rows = xs[edge[e]:edge[e + 1]]
+        gq.hessian_accumulate(H, rows)
+        r64 = rows.double().cpu().numpy()
+        low = np.tril_indices(K)
+        ref = (r64.T @ r64)[low]
+        assert np.linalg.norm(H.double().cpu().numpy()[low] - ref) <= 1e-5 * np.linalg.norm(ref)
+        gq.gptq_quantize(codes[e], scales[e], W[e], H, None, G, 0.01,
+                         gq.workspace(gq.gptq_quantize_workspace_size(N, K, G), DEV))
+        gq.fp8_quantize(wq[e], ws[e], W[e], 128)
+    y4 = torch.zeros(T * k, N, device=DEV)
+    gq.int4_matmul_experts(y4, xs, codes, scales, off, G)
+    xq, xsc = torch.empty(T * k, K, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(T * k, K // 128, device=DEV)
+    gq.fp8_quantize(xq, xsc, xs, 1)
+    y8 = torch.zeros(T * k, N, device=DEV)
+    gq.fp8_matmul_experts(y8, xq, xsc, wq, ws, off)
+    full = torch.zeros(T * k, N, dtype=torch.float64)
+    for e in range(E):
+        full[edge[e]:edge[e + 1]] = xs[edge[e]:edge[e + 1]].double().cpu() @ W[e].double().cpu().T
+    # int4 GPTQ is some 8% off in the weights on these sizes, e4m3 on both sides some 4%: both well inside 15% and 6%
+    assert (y4[:kept].double().cpu() - full[:kept]).norm() < 0.15 * full[:kept].norm()
+    assert (y8[:kept].double().cpu() - full[:kept]).norm() < 0.06 * full[:kept].norm()
+    w = torch.softmax(torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)), 1).to(DEV)
+    out = torch.empty(T, N, device=DEV)
+    gq.experts_combine(out, y4, pos, w)
+    p, w64, y64 = pos.cpu(), w.double().cpu(), y4.double().cpu()
+    live = (p >= 0).double()
+    ref = (w64 * live).unsqueeze(2) * y64[p.clamp_min(0).long()]
+    assert ((out.double().cpu() - ref.sum(1)).abs() <= 3 * 2.0 ** -24 * ref.abs().sum(1) * (1 + 2.0 ** -23)).all()
+    g = torch.from_numpy(rng.standard_normal((T, N)).astype(np.float32)).to(DEV)
+    dy, dw = torch.zeros(T * k, N, device=DEV), torch.empty(T, k, device=DEV)
+    gq.experts_combine_backward(dy, dw, g, y4, pos, w)
+    terms = g.double().cpu().unsqueeze(1) * y64[p.clamp_min(0).long()] * live.unsqueeze(2)
+    assert ((dw.double().cpu() - terms.sum(2)).abs() <= (N + 1) * 2.0 ** -24 * terms.abs().sum(2)).all()
