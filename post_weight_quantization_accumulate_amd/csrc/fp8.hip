@@ -151,8 +151,167 @@ template <typename TY, bool VEC> __global__ __launch_bounds__(64 * kWaves) void 
     if (rt.r0 + row < rt.r1 && n0 + col < a.N) store_y((TY *)a.Y + (rt.r0 + row) * a.ldy + n0 + col, v);
 }
 
+// ---------------------------------------------------------------- large tiles
+// WM x WN waves, each PM x PN blocks of 16 x 16: TM = 16 WM PM rows by TN = 16
+// WN PN columns of Y per workgroup, one block of 128 k per stage, two stages in
+// LDS: while one is multiplied the next is copied into the other.  Row rho of an
+// operand's stage is 128 bytes, its 16-byte chunk c at position c ^ (rho & 7):
+// 8 lanes that read one chunk of 8 rows meet 8 different positions.
+//
+// v_mfma_f32_16x16x128_f8f6f4 covers exactly one scale block: lane l feeds the
+// codes k = 32 (l / 16) + 0..31 of row l % 16 of each operand, and the weights go
+// first, so a lane's 4 results are columns 4 (l / 16) + 0..3 of row l % 16 of Y
+// and share one scale xs[m] ws[n / 128].  The scaled sums must be in VGPRs (the
+// matrix cores alone reach the AGPRs), so a wave holds at most 128 of them.
+// With F8 false (fp32 outputs) the codes are turned into bf16 instead.
+constexpr int kStage = 128;
+
+template <typename TY, int WM, int WN, int PM, int PN, bool DMA, bool F8>
+__global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(F8Args a, int64_t nt, int64_t mt)
+{
+    constexpr int NW = WM * WN, TM = 16 * WM * PM, TN = 16 * WN * PN, ROWS = TM + TN;
+    static_assert(kBlock % (16 * PN) == 0 && ROWS % (8 * NW) == 0 && TM % 64 == 0 && TM / 64 <= NW, "tile");
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    constexpr int kSlot = ROWS * kStage;
+    float *sxl = (float *)(lds + 2 * kSlot);             // 2 x TM
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int64_t ti, tj;
+    grouped_tile(blockIdx.x, nt, mt, ti, tj);
+    RowTile rt;
+    if (!row_tile(a.offsets, (int)a.E, a.M, TM, ti, rt)) return;
+    const int n0 = (int)tj * TN;
+    const int K = a.K, kb = a.kb;
+    const uint8_t *xbase = a.Xq + rt.r0 * K;
+    const uint8_t *wbase = a.Wq + (rt.e * a.N + n0) * (int64_t)K;
+    const int mrows = (int)(rt.r1 - rt.r0), nrows = min(TN, a.N - n0);
+    const float *sxbase = a.xs + rt.r0 * kb;
+    const int wm = wave % WM, wn = wave / WM;
+    const float *sw = a.ws + (rt.e * ((a.N + kBlock - 1) / kBlock) + min(n0 + 16 * PN * wn, a.N - 1) / kBlock) * (int64_t)kb;
+
+    // copy u of this wave: 8 rows (8 (wave + NW u) ...) of the tile's TM + TN;
+    // lane l takes position l % 8 of row l / 8.  Rows past the end repeat the last.
+    constexpr int NC = ROWS / (8 * NW);
+    unsigned off[NC];
+    const unsigned ch = 16u * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+    for (int u = 0; u < NC; ++u) {
+        const int row = 8 * (wave + NW * u) + (lane >> 3);
+        off[u] = (unsigned)(row < TM ? min(row, mrows - 1) : min(row - TM, nrows - 1)) * (unsigned)K + ch;
+    }
+    const unsigned lbase = lds_offset(lds);
+    auto copy = [&](int b, int slot) {
+        if (DMA && b * kStage + kStage <= K) {
+#pragma unroll
+            for (int u = 0; u < NC; ++u) {
+                const int r8 = 8 * (wave + NW * u);
+                copy16_lds((r8 < TM ? xbase : wbase) + b * kStage, off[u], lbase + slot * kSlot + r8 * kStage);
+            }
+        } else {
+            const int left = K - b * kStage - (int)ch;
+#pragma unroll
+            for (int u = 0; u < NC; ++u) {
+                const int r8 = 8 * (wave + NW * u);
+                *(u32x4 *)(lds + slot * kSlot + r8 * kStage + 16 * lane) =
+                    load16((r8 < TM ? xbase : wbase) + b * kStage + off[u], left);
+            }
+        }
+        if (wave < TM / 64)
+            copy4_lds(sxbase + b, 4u * (unsigned)(min(64 * wave + lane, mrows - 1) * kb), lds_offset(sxl) + 4u * (slot * TM + 64 * wave));
+    };
+
+    const int r = lane & 15, q = lane >> 4;
+    const int rd0 = r * kStage + 16 * ((2 * q) ^ (r & 7)), rd1 = r * kStage + 16 * ((2 * q + 1) ^ (r & 7));
+    f32x4 acc[PM][PN];
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int j = 0; j < PN; ++j) acc[i][j] = f32x4{};
+    struct Frag { u32x4 lo, hi; };
+    auto read = [&](const uint8_t *p) { return Frag{*(const u32x4 *)(p + rd0), *(const u32x4 *)(p + rd1)}; };
+    auto product = [&](const Frag &w, const Frag &x) {
+        f32x4 part{};
+        if constexpr (F8) {
+            typedef int i32x8 __attribute__((ext_vector_type(8)));
+            part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, w), __builtin_bit_cast(i32x8, x),
+                                                                    part, 0, 0, 0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const u32x4 &wv = h < 2 ? w.lo : w.hi, &xv = h < 2 ? x.lo : x.hi;
+                const int i = 2 * (h & 1);
+                part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_fp8(wv[i], wv[i + 1]), bf16_of_fp8(xv[i], xv[i + 1]),
+                                                               part, 0, 0, 0);
+            }
+        }
+        return part;
+    };
+
+    copy(0, 0);
+    for (int b = 0; b < kb; ++b) {
+        const int slot = b & 1;
+        publish();
+        if (b + 1 < kb) copy(b + 1, slot ^ 1);
+        const uint8_t *xs_ = lds + slot * kSlot + 16 * PM * wm * kStage;
+        const uint8_t *ws_ = lds + slot * kSlot + (TM + 16 * PN * wn) * kStage;
+        const float s_w = sw[b];
+        Frag w[PN];
+#pragma unroll
+        for (int j = 0; j < PN; ++j) w[j] = read(ws_ + 16 * j * kStage);
+#pragma unroll
+        for (int i = 0; i < PM; ++i) {
+            const Frag x = read(xs_ + 16 * i * kStage);
+            const float s = sxl[slot * TM + 16 * (PM * wm + i) + r] * s_w;
+            f32x4 part[PN];
+#pragma unroll
+            for (int j = 0; j < PN; ++j) part[j] = product(w[j], x);
+#pragma unroll
+            for (int j = 0; j < PN; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(s, part[j][t], acc[i][j][t]);
+        }
+    }
+    const bool v4 = a.ldy % 4 == 0 && ((uintptr_t)a.Y & (4 * sizeof(TY) - 1)) == 0;
+#pragma unroll
+    for (int i = 0; i < PM; ++i) {
+        const int64_t row = rt.r0 + 16 * (PM * wm + i) + r;
+        if (row >= rt.r1) continue;
+        TY *y = (TY *)a.Y + row * a.ldy;
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+            const int n = n0 + 16 * (PN * wn + j) + 4 * q;
+            if (v4 && n + 4 <= a.N) {
+                typedef TY y4 __attribute__((ext_vector_type(4)));
+                y4 o;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) o[t] = (TY)acc[i][j][t];
+                *(y4 *)(y + n) = o;
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (n + t < a.N) y[n + t] = (TY)acc[i][j][t];
+            }
+        }
+    }
+}
+
+template <typename TY, int WM, int WN, int PM, int PN, bool DMA>
+hipError_t launch_tile(const F8Args &a, hipStream_t s)
+{
+    constexpr int TM = 16 * WM * PM, TN = 16 * WN * PN;
+    constexpr size_t lds = 2 * ((size_t)(TM + TN) * kStage + TM * sizeof(float));
+    const auto kernel = fp8_tile_kernel<TY, WM, WN, PM, PN, DMA, sizeof(TY) == 2>;
+    static const bool lds_ok = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
+    if (!lds_ok) return hipErrorInvalidConfiguration;
+    const int64_t nt = (a.N + TN - 1) / TN, mt = row_tiles(a.offsets != nullptr, a.E, a.M, TM);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(nt * mt)), dim3(64 * WM * WN), lds, s, a, nt, mt);
+    return hipGetLastError();
+}
+
 template <typename TY> hipError_t launch_fp8(F8Args a, hipStream_t s)
 {
+    const bool dma = a.K % 16 == 0 && ((uintptr_t)a.Xq & 15) == 0 && ((uintptr_t)a.Wq & 15) == 0;
+    if (a.M > 64 && a.K <= (1 << 22)) return dma ? launch_tile<TY, 2, 4, 8, 4, true>(a, s) : launch_tile<TY, 2, 4, 8, 4, false>(a, s);
     const dim3 grid = tile_grid((a.N + 15) / 16, row_tiles(a.offsets != nullptr, a.E, a.M, 16));
     const bool vec = a.K % 8 == 0 && ((uintptr_t)a.Xq & 7) == 0 && ((uintptr_t)a.Wq & 7) == 0;
     if (vec) hipLaunchKernelGGL((fp8_direct_kernel<TY, true>), grid, dim3(64 * kWaves), 0, s, a);

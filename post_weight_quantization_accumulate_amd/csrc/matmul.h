@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gq_internal.h"
+
 namespace gq {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -50,11 +52,11 @@ __device__ inline bool row_tile(const int *offsets, int E, int64_t M, int TM, in
             const int v = __shfl_up(inc, d);
             if (lane >= d) inc += v;
         }
-        const int total = __shfl(inc, 63);
+        const int total = __builtin_amdgcn_readlane(inc, 63);
         if (want < total) {
             const int f = __builtin_ctzll(__ballot(inc > want));
-            const int first = __shfl(inc - nt, f);
-            const int elo = __shfl(lo, f), ehi = __shfl(hi, f);
+            const int first = __builtin_amdgcn_readlane(inc - nt, f);
+            const int elo = __builtin_amdgcn_readlane(lo, f), ehi = __builtin_amdgcn_readlane(hi, f);
             out.r0 = elo + (int64_t)(want - first) * TM;
             out.r1 = min(out.r0 + TM, (int64_t)ehi);
             out.e = base + f;
@@ -100,6 +102,56 @@ __device__ inline void split3(float v, unsigned short &h, unsigned short &m, uns
     h = (unsigned short)(hb >> 16);
     m = (unsigned short)(mb >> 16);
     l = (unsigned short)(__float_as_uint(q) >> 16);
+}
+
+// Workgroup `w` of nt x mt tiles: each XCD gets a contiguous run of tiles (see
+// xcd_order), which walk the grid in groups of kGroupRows row tiles, so that the
+// tiles that run together on one XCD share their operands in its L2.
+constexpr int64_t kGroupRows = 8;
+__device__ inline void grouped_tile(int64_t w, int64_t nt, int64_t mt, int64_t &ti, int64_t &tj)
+{
+    const int64_t id = xcd_order(w, nt * mt);
+    const int64_t g = id / (kGroupRows * nt), first = g * kGroupRows;
+    const int64_t rows = min(kGroupRows, mt - first), in = id - first * nt;
+    ti = first + in % rows;
+    tj = in / rows;
+}
+
+// 64 lanes x 16 (or 4) bytes from base + off (off per lane) to LDS at l + 16
+// (4) lane, past the registers.  Inline asm, so that the compiler does not wait
+// for every copy before any LDS read: the caller waits with wait_copies before
+// the barrier that publishes them.  M0 is set right before each copy and used
+// by nothing else.
+__device__ inline void copy16_lds(const void *base, unsigned off, unsigned l)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(l) : "memory");
+}
+__device__ inline void copy4_lds(const void *base, unsigned off, unsigned l)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(l) : "memory");
+}
+__device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ inline void publish()
+{
+    wait_copies();
+    __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): this wave's LDS writes
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+__device__ inline unsigned lds_offset(const void *p)
+{
+    return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+// 16 bytes from p, of which only the first n are the caller's (the rest zero);
+// p may be unaligned.
+__device__ inline u32x4 load16(const uint8_t *p, int n)
+{
+    u32x4 v{};
+    if (n >= 16) __builtin_memcpy(&v, p, 16);
+    else
+        for (int i = 0; i < n; ++i) v[i >> 2] |= (unsigned)p[i] << (8 * (i & 3));
+    return v;
 }
 
 __device__ inline void store_y(float *p, float v) { *p = v; }
