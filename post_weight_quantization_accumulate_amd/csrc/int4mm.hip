@@ -156,8 +156,154 @@ hipError_t launch_direct(const I4Args &a, bool vec, dim3 grid, hipStream_t s)
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------- large tiles, bf16 X
+// Eight codes of one dword as bf16, exactly: a byte holding a code in its high
+// nibble is 16 code as a signed byte, one conversion per code; the factor 1/16
+// goes with the scale.
+__device__ inline bf16x8 bf16_of_int4(unsigned w)
+{
+    const unsigned lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
+    bf16x8 r;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        r[2 * t] = (__bf16)(float)(signed char)(lo >> (8 * t));
+        r[2 * t + 1] = (__bf16)(float)(signed char)(hi >> (8 * t));
+    }
+    return r;
+}
+
+constexpr int kStage = 128;                 // k per stage
+
+// WM x WN waves of PM x PN blocks of 16 x 16.
+template <typename TY, int WM, int WN, int PM, int PN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void int4_tile_kernel(I4Args a, int64_t nt, int64_t mt)
+{
+    constexpr int NW = WM * WN, TM = 16 * WM * PM, TN = 16 * WN * PN, kRow = 2 * kStage;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    constexpr int kSlot = TM * kRow;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int64_t ti, tj;
+    grouped_tile(blockIdx.x, nt, mt, ti, tj);
+    RowTile rt;
+    if (!row_tile(a.offsets, (int)a.E, a.M, TM, ti, rt)) return;
+    const int n0 = (int)tj * TN, K = a.K;
+    const int mrows = (int)(rt.r1 - rt.r0);
+    const uint8_t *xbase = (const uint8_t *)((const __bf16 *)a.X + rt.r0 * a.ldx);
+    const int wm = wave % WM, wn = wave / WM;
+    const int r = lane & 15, q = lane >> 4;
+
+    // copy u: rows 4 wave + 4 NW u .. + 3, 256 bytes each; lane l takes position
+    // l % 16 of row l / 16, chunk position ^ (row & 15).  The offsets are formed
+    // at each copy: kept, they would not fit the registers beside the sums.
+    constexpr int NC = TM / (4 * NW);
+    static_assert((4 * NW) % 16 == 0, "row & 15 is the same for every u");
+    int crow = 4 * wave + (lane >> 4);
+    const unsigned ch = 16u * ((lane & 15) ^ (crow & 15));
+    const unsigned ld2 = (unsigned)(2 * a.ldx);
+    const unsigned lbase = lds_offset(lds);
+    auto copy = [&](int b, int slot) {
+        asm volatile("" : "+v"(crow));
+#pragma unroll
+        for (int u = 0; u < NC; ++u) {
+            copy16_lds(xbase + 256 * b, (unsigned)min(crow + 4 * NW * u, mrows - 1) * ld2 + ch, lbase + slot * kSlot + 4 * (wave + NW * u) * kRow);
+        }
+    };
+    const uint8_t *cbase = a.codes + (rt.e * a.N + n0) * (int64_t)(K / 2);
+    const int nb = K / kStage;
+    const float *sbase = a.scales + (rt.e * a.N + n0) * (int64_t)(K / a.G);
+    const int nlast = a.N - n0 - 1;
+    int nrow = 16 * PN * wn + r;
+    u32x4 cn[PN];
+    float sn[PN];
+    auto load_w = [&](int b) {
+        const uint8_t *cb = cbase + 64 * b;
+        const float *sb = sbase + b;
+        asm volatile("" : "+v"(nrow));
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+            const unsigned n = (unsigned)min(nrow + 16 * j, nlast);
+            cn[j] = *(const u32x4 *)(cb + (n * (unsigned)(K / 2) + 16u * q));
+            sn[j] = *(const float *)((const uint8_t *)sb + n * (unsigned)(4 * nb));
+        }
+    };
+    f32x4 acc[PM][PN];
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int j = 0; j < PN; ++j) acc[i][j] = f32x4{};
+    copy(0, 0);
+    load_w(0);
+    const int rx = r * kRow;
+    for (int b = 0; b < nb; ++b) {
+        const int slot = b & 1;
+        publish();
+        bf16x8 w[PN][4];
+        float s[PN];
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) w[j][h] = bf16_of_int4(cn[j][h]);
+            s[j] = sn[j] * 0.0625f;
+        }
+        if (b + 1 < nb) {
+            copy(b + 1, slot ^ 1);
+            load_w(b + 1);
+        }
+        const uint8_t *xs = lds + slot * kSlot + 16 * PM * wm * kRow + rx;
+#pragma unroll
+        for (int i = 0; i < PM; ++i) {
+            bf16x8 x[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) x[h] = *(const bf16x8 *)(xs + 16 * i * kRow + 16 * ((4 * q + h) ^ r));
+#pragma unroll
+            for (int j0 = 0; j0 < PN; j0 += 2) {
+                f32x4 part[2] = {};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[h], w[j0 + j][h], part[j], 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[i][j0 + j][t] = fmaf(s[j0 + j], part[j][t], acc[i][j0 + j][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t row = rt.r0 + 16 * (PM * wm + i) + 4 * q + t;
+            if (row >= rt.r1) continue;
+            TY *y = (TY *)a.Y + row * a.ldy;
+#pragma unroll
+            for (int j = 0; j < PN; ++j) {
+                const int n = n0 + 16 * (PN * wn + j) + r;
+                if (n < a.N) store_y(y + n, acc[i][j][t]);
+            }
+        }
+}
+
+template <typename TY, int WM, int WN, int PM, int PN> hipError_t launch_tile(const I4Args &a, hipStream_t s)
+{
+    constexpr int TM = 16 * WM * PM, TN = 16 * WN * PN;
+    constexpr size_t lds = 2 * (size_t)TM * 2 * kStage;
+    const auto kernel = int4_tile_kernel<TY, WM, WN, PM, PN>;
+    static const bool lds_ok = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
+    if (!lds_ok) return hipErrorInvalidConfiguration;
+    const int64_t nt = (a.N + TN - 1) / TN, mt = row_tiles(a.offsets != nullptr, a.E, a.M, TM);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(nt * mt)), dim3(64 * WM * WN), lds, s, a, nt, mt);
+    return hipGetLastError();
+}
+
 template <typename TX, typename TY> hipError_t launch_int4(I4Args a, bool nf4, hipStream_t s)
 {
+    if constexpr (sizeof(TX) == 2) {
+        if (a.M > 64 && !nf4 && a.G == 128 && a.ldx % 8 == 0 && a.ldx <= (1 << 22) && ((uintptr_t)a.X & 15) == 0 && ((uintptr_t)a.codes & 15) == 0)
+            return launch_tile<TY, 1, 4, 8, 4>(a, s);
+    }
     const dim3 grid = tile_grid((a.N + 15) / 16, row_tiles(a.offsets != nullptr, a.E, a.M, 16));
     const bool vec = a.K % 8 == 0 && ((uintptr_t)a.X & 15) == 0 && (a.ldx * sizeof(TX)) % 16 == 0 &&
                      ((uintptr_t)a.codes & 3) == 0;
