@@ -1,0 +1,190 @@
+// int4_tile.hip -- int4 / NF4 pack products of many rows.
+//
+// Four waves side by side, each PM x PN blocks of 16 x 16 of Y: TM = 16 PM rows by
+// TN = 64 PN columns per workgroup, two workgroups to a CU.  A stage is 256 bytes
+// of each row of X (128 k of bf16, 64 of fp32), two stages in LDS, the next
+// copied past the registers while one is multiplied.  Every wave reads the whole
+// X tile and turns only its own columns' codes into bf16, in registers: the codes
+// never go through LDS, and a code is converted once per TM rows.  Row rho of a
+// stage is 16 chunks of 16 bytes, chunk c at position c ^ (rho & 15), so 8 lanes
+// that read one chunk of 8 rows meet 8 different positions.
+//
+// v_mfma_f32_16x16x32_bf16 takes 8 k from each lane; which k is free as long as X
+// and W agree.  Where a stage lies inside one group (NG = 1) lane l / 16 = q takes
+// k = (KS / 4) q + 8 h of step h, so that its codes of the whole stage are one
+// load; with NG groups per stage step h has to lie in one group and takes
+// k = 32 h + 8 q.  A group's sum is formed apart and multiplied by its scale.
+#include "int4mm.h"
+
+namespace gq {
+namespace {
+
+constexpr int kRow = 256;                   // bytes of X per row and stage
+
+template <typename TX, int WMODE, int NG, int PM, int PN>
+__global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a, int64_t nt, int64_t mt, bool dma)
+{
+    constexpr int NW = 4, TM = 16 * PM, TN = 16 * NW * PN, KS = kRow / (int)sizeof(TX), NH = KS / 32;
+    constexpr int kSlot = TM * kRow, NC = TM / (4 * NW), PX = XParts<TX>::n, PW = WParts<WMODE>::n;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    __shared__ Nf4Table tab;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if constexpr (WMODE != W_INT4) tab.fill();
+    int64_t ti, tj;
+    grouped_tile(blockIdx.x, nt, mt, ti, tj);
+    RowTile rt;
+    if (!row_tile(a.offsets, (int)a.E, a.M, TM, ti, rt)) return;
+    const int n0 = (int)tj * TN, K = a.K;
+    const int mrows = (int)(rt.r1 - rt.r0);
+    const uint8_t *xbase = (const uint8_t *)((const TX *)a.X + rt.r0 * a.ldx);
+    const int r = lane & 15, q = lane >> 4;
+
+    // copy u: rows 4 wave + 16 u .. + 3; lane l takes position l % 16 of row
+    // l / 16.  The offsets are formed at each copy: kept, they would not fit the
+    // registers beside the sums.  Rows past the end repeat the last.
+    int crow = 4 * wave + q;
+    const unsigned ch = 16u * (r ^ (crow & 15));
+    const unsigned ld = (unsigned)(a.ldx * (int64_t)sizeof(TX));
+    const unsigned lbase = lds_offset(lds);
+    const int kbytes = K * (int)sizeof(TX);
+    auto copy = [&](int b, int slot) {
+        asm volatile("" : "+v"(crow));
+        if (dma && (b + 1) * kRow <= kbytes) {
+#pragma unroll
+            for (int u = 0; u < NC; ++u)
+                copy16_lds(xbase + kRow * b, (unsigned)min(crow + 16 * u, mrows - 1) * ld + ch,
+                           lbase + slot * kSlot + (4 * wave + 16 * u) * kRow);
+        } else {
+            // rows that do not start on 16 bytes, or the end of a row: through registers, zero past K
+#pragma unroll
+            for (int u = 0; u < NC; ++u)
+                *(u32x4 *)(lds + slot * kSlot + (4 * wave + 16 * u) * kRow + 16 * lane) =
+                    load16(xbase + kRow * b + ((unsigned)min(crow + 16 * u, mrows - 1) * ld + ch), kbytes - kRow * b - (int)ch);
+        }
+    };
+
+    const uint8_t *cbase = a.codes + (rt.e * a.N + n0) * (int64_t)(K / 2);
+    const int ngroups = K / a.G, lg = __builtin_ctz(a.G);
+    const float *sbase = a.scales + (rt.e * a.N + n0) * (int64_t)ngroups;
+    const int nlast = a.N - n0 - 1;
+    int nrow = 16 * PN * wave + r;
+    unsigned cn[PN][NH];
+    float sn[PN][NG];
+    auto load_w = [&](int b) {
+        asm volatile("" : "+v"(nrow));
+        // past K: any codes of the row (X is zero there)
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+            const unsigned n = (unsigned)min(nrow + 16 * j, nlast);
+            const uint8_t *c = cbase + n * (unsigned)(K / 2);
+            if constexpr (NG == 1) {
+                __builtin_memcpy(&cn[j][0], c + min((KS / 2) * b + (KS / 8) * q, K / 2 - KS / 8), KS / 8);
+            } else {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) __builtin_memcpy(&cn[j][h], c + min((KS / 2) * b + 16 * h + 4 * q, K / 2 - 4), 4);
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) sn[j][g] = sbase[n * (unsigned)ngroups + min((b * KS + g * (KS / NG)) >> lg, ngroups - 1)];
+        }
+    };
+    f32x4 acc[PM][PN];
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int j = 0; j < PN; ++j) acc[i][j] = f32x4{};
+    const int nb = (K + KS - 1) / KS;
+    copy(0, 0);
+    load_w(0);
+    for (int b = 0; b < nb; ++b) {
+        const int slot = b & 1;
+        publish();
+        bf16x8 w[PN][NH][PW];
+        float s[PN][NG];
+#pragma unroll
+        for (int j = 0; j < PN; ++j) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) code_parts<WMODE>(cn[j][h], tab, w[j][h]);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) s[j][g] = sn[j][g] * (1.0f / CodeScale<WMODE>::v);
+        }
+        if (b + 1 < nb) {
+            copy(b + 1, slot ^ 1);
+            load_w(b + 1);
+        }
+        const uint8_t *xs = lds + slot * kSlot + r * kRow;
+#pragma unroll
+        for (int i = 0; i < PM; ++i) {
+            bf16x8 x[NH][PX];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                // element of the row's stage at which this lane's 8 begin, and its chunk
+                const int k0 = NG == 1 ? (KS / 4) * q + 8 * h : 32 * h + 8 * q;
+                const int c = k0 * (int)sizeof(TX) / 16;
+                x_parts((const TX *)(xs + 16 * i * kRow + 16 * (c ^ r)), (const TX *)(xs + 16 * i * kRow + 16 * ((c + 1) ^ r)), x[h]);
+            }
+#pragma unroll
+            for (int j0 = 0; j0 < PN; j0 += 2)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    f32x4 part[2] = {};
+#pragma unroll
+                    for (int h = g * (NH / NG); h < (g + 1) * (NH / NG); ++h)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) part[j] = mma_parts(x[h], w[j0 + j][h], part[j]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) acc[i][j0 + j][t] = fmaf(s[j0 + j][g], part[j][t], acc[i][j0 + j][t]);
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t row = rt.r0 + 16 * i + 4 * q + t;
+            if (row >= rt.r1) continue;
+#pragma unroll
+            for (int j = 0; j < PN; ++j) {
+                const int n = n0 + 16 * (PN * wave + j) + r;
+                if (n < a.N) store_row(a, row, n, acc[i][j][t]);
+            }
+        }
+}
+
+template <typename TX, int WMODE, int NG, int PM, int PN> hipError_t launch(const I4Args &a, hipStream_t s)
+{
+    constexpr int TM = 16 * PM, TN = 64 * PN;
+    constexpr size_t lds = 2 * (size_t)TM * kRow;
+    const auto kernel = int4_tile_kernel<TX, WMODE, NG, PM, PN>;
+    static const bool lds_ok =
+        hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
+    if (!lds_ok) return hipErrorInvalidConfiguration;
+    const bool dma = ((uintptr_t)a.X & 15) == 0 && (a.ldx * sizeof(TX)) % 16 == 0;
+    const int64_t nt = (a.N + TN - 1) / TN, mt = row_tiles(a.offsets != nullptr, a.E, a.M, TM);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(nt * mt)), dim3(256), lds, s, a, nt, mt, dma);
+    return hipGetLastError();
+}
+
+// The weights' bf16 parts of a stage stay in registers beside the sums: 64
+// columns per wave fit with one part and up to two scales per stage, else 32.
+template <typename TX, int WMODE> hipError_t by_group(const I4Args &a, hipStream_t s)
+{
+    constexpr int KS = kRow / (int)sizeof(TX), PN = WMODE == W_INT4 ? 4 : 2;
+    if (a.G >= KS) return launch<TX, WMODE, 1, 8, PN>(a, s);
+    if (2 * a.G == KS) return launch<TX, WMODE, 2, 8, PN>(a, s);
+    if constexpr (KS == 128) return launch<TX, WMODE, 4, 8, 2>(a, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s)
+{
+    if (!x_bf16) return nf4 ? by_group<float, W_NF4_3>(a, s) : by_group<float, W_INT4>(a, s);
+    if (!nf4) return by_group<__bf16, W_INT4>(a, s);
+    return a.y_bf16 ? by_group<__bf16, W_NF4_2>(a, s) : by_group<__bf16, W_NF4_3>(a, s);
+}
+
+}  // namespace gq

@@ -1,0 +1,116 @@
+// int4mm.h -- shared parts of the int4 / NF4 pack products: the arguments, codes
+// to bf16, activations to bf16 parts.
+#pragma once
+
+#include "gq_internal.h"
+#include "matmul.h"
+
+namespace gq {
+
+struct I4Args {
+    void *Y;
+    const void *X;
+    const uint8_t *codes;
+    const float *scales;
+    const int *offsets;
+    int64_t M, ldx, ldy, E;
+    int N, K, G;
+    bool y_bf16;
+};
+
+// How a pack's codes enter the bf16 matrix cores.
+//   W_INT4  the code itself, exactly, in one bf16;
+//   W_NF4   its level (fp32) as two or three bf16 parts: two (16 leading bits,
+//           2^-16 off at most) where the result is rounded to bf16 anyway.
+enum : int { W_INT4 = 0, W_NF4_2 = 2, W_NF4_3 = 3 };
+template <int WM> struct WParts { static constexpr int n = WM == W_INT4 ? 1 : WM; };
+
+// The NF4 levels' bf16 parts, for an LDS table of 16 entries (first part in the
+// low half of .x, second in the high half, third in .y).  16 entries lie in 16
+// (.x alone) or 32 banks: lanes with different codes never meet in one.
+struct Nf4Table {
+    uint2 e[16];
+    __device__ void fill()
+    {
+        if (threadIdx.x < 16) {
+            unsigned short h, m, l;
+            split3(kNF4[threadIdx.x], h, m, l);
+            e[threadIdx.x] = make_uint2(h | (unsigned)m << 16, l);
+        }
+    }
+};
+
+// Eight codes of one dword (code t in bits 4t ..) as the PW bf16 parts of
+// kCodeScale times their values.  int4: a byte holding a code in its high nibble
+// is 16 times the code as a signed byte, one conversion each; the factor is taken
+// out of the scale.
+template <int WM> struct CodeScale { static constexpr float v = WM == W_INT4 ? 16.0f : 1.0f; };
+template <int WM> __device__ inline void code_parts(unsigned w, const Nf4Table &tab, bf16x8 (&p)[WParts<WM>::n])
+{
+    if constexpr (WM == W_INT4) {
+        const unsigned lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            p[0][2 * t] = (__bf16)(float)(signed char)(lo >> (8 * t));
+            p[0][2 * t + 1] = (__bf16)(float)(signed char)(hi >> (8 * t));
+        }
+    } else {
+        u32x4 o[WM];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int c0 = (w >> (8 * t)) & 15, c1 = (w >> (8 * t + 4)) & 15;
+            const unsigned a = tab.e[c0].x, b = tab.e[c1].x;
+            o[0][t] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            o[1][t] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+            if constexpr (WM == W_NF4_3) o[2][t] = __builtin_amdgcn_perm(tab.e[c1].y, tab.e[c0].y, 0x05040100u);
+        }
+#pragma unroll
+        for (int j = 0; j < WM; ++j) p[j] = __builtin_bit_cast(bf16x8, o[j]);
+    }
+}
+
+// Eight consecutive elements of X from memory or LDS (16-byte pieces) as bf16 parts.
+template <typename TX> struct XParts { static constexpr int n = sizeof(TX) == 4 ? 3 : 1; };
+__device__ inline void x_parts(const __bf16 *p0, const __bf16 *, bf16x8 (&p)[1]) { p[0] = *(const bf16x8 *)p0; }
+__device__ inline void x_parts(f32x4 a, f32x4 b, bf16x8 (&p)[3])
+{
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        unsigned short h, m, l;
+        split3(v[t], h, m, l);
+        p[0][t] = __builtin_bit_cast(__bf16, h);
+        p[1][t] = __builtin_bit_cast(__bf16, m);
+        p[2][t] = __builtin_bit_cast(__bf16, l);
+    }
+}
+// p0, p1: the two 16-byte halves (4 elements each)
+__device__ inline void x_parts(const float *p0, const float *p1, bf16x8 (&p)[3])
+{
+    x_parts(*(const f32x4 *)p0, *(const f32x4 *)p1, p);
+}
+
+// part += sum over the parts i of X and j of W with i + j <= 2: what is left out
+// is below 2^-24 of each product.
+template <int PX, int PW> __device__ inline f32x4 mma_parts(const bf16x8 (&x)[PX], const bf16x8 (&w)[PW], f32x4 part)
+{
+#pragma unroll
+    for (int i = 0; i < PX; ++i)
+#pragma unroll
+        for (int j = 0; j < PW; ++j)
+            if (i + j <= 2) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], w[j], part, 0, 0, 0);
+    return part;
+}
+
+__device__ inline void store_row(const I4Args &a, int64_t row, int n, float v)
+{
+    if (a.y_bf16) ((__bf16 *)a.Y)[row * a.ldy + n] = (__bf16)v;
+    else ((float *)a.Y)[row * a.ldy + n] = v;
+}
+
+// Groups of 32 and more, any M, K, strides and alignment (int4_tile.hip).
+hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s);
+// The same for few rows (int4_skinny.hip).
+hipError_t launch_int4_skinny(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s);
+
+}  // namespace gq

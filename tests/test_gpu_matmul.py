@@ -76,7 +76,8 @@ def _int4(gq, M, N, K, G, nf4, xd, yd, seed, padx=0, pady=0):
 @pytest.mark.parametrize("M,N,K,G", [(1, 64, 128, 32), (1, 10, 6, 2), (3, 33, 96, 32), (17, 100, 130, 1),
                                      (16, 48, 640, 128), (64, 256, 1024, 128), (65, 300, 192, 64), (130, 257, 256, 16),
                                      (300, 130, 512, 128), (257, 515, 2176, 128), (5, 16, 2, 1), (2, 1000, 5120, 128),
-                                     (33, 272, 1152, 128), (600, 520, 384, 128)])
+                                     (33, 272, 1152, 128), (600, 520, 384, 128), (100, 70, 160, 32), (129, 65, 32, 32),
+                                     (200, 129, 320, 64), (20, 40, 224, 32), (50, 40, 320, 64)])
 def test_int4_matmul(gq, M, N, K, G, nf4, xd, yd):
     _int4(gq, M, N, K, G, nf4, xd, yd, M * 31 + N + K)
 
