@@ -2,6 +2,7 @@
 // columns, and products of two of them.
 #include "gq.h"
 #include "gq_internal.h"
+#include "gemv.h"
 #include "matmul.h"
 
 namespace gq {
@@ -311,6 +312,13 @@ hipError_t launch_tile(const F8Args &a, hipStream_t s)
 template <typename TY> hipError_t launch_fp8(F8Args a, hipStream_t s)
 {
     const bool dma = a.K % 16 == 0 && ((uintptr_t)a.Xq & 15) == 0 && ((uintptr_t)a.Wq & 15) == 0;
+    GemvArgs v{};
+    v.Y = a.Y; v.X = a.Xq; v.xs = a.xs; v.codes = a.Wq; v.scales = a.ws; v.offsets = a.offsets;
+    v.M = a.M; v.ldx = a.K; v.ldy = a.ldy; v.E = a.E;
+    v.N = a.N; v.K = a.K; v.G = kBlock;
+    v.y_bf16 = sizeof(TY) == 2;
+    const int64_t rows = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
+    if (rows <= kGemvMaxRows && gemv_ok(v, GEMV_FP8, (int)rows)) return launch_gemv(v, GEMV_FP8, (int)rows, s);
     if (a.M > 64 && a.K <= (1 << 22)) return dma ? launch_tile<TY, 2, 4, 8, 4, true>(a, s) : launch_tile<TY, 2, 4, 8, 4, false>(a, s);
     const dim3 grid = tile_grid((a.N + 15) / 16, row_tiles(a.offsets != nullptr, a.E, a.M, 16));
     const bool vec = a.K % 8 == 0 && ((uintptr_t)a.Xq & 7) == 0 && ((uintptr_t)a.Wq & 7) == 0;

@@ -69,6 +69,21 @@ template <int WM> __device__ inline void code_parts(unsigned w, const Nf4Table &
     }
 }
 
+// Transposes a 4 x 4 array of dwords whose column is the lane's group of 16
+// (q = lane / 16) and whose row is the register: d[h] of group q becomes d[q] of
+// group h.  Loads want 16 consecutive bytes of codes per lane, and a matrix
+// instruction that has to stay within a group wants 32 consecutive k over the four
+// groups of lanes: this turns one into the other.
+__device__ inline void transpose4(unsigned (&d)[4])
+{
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+    u32x2 b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+    u32x2 c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    u32x2 e = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    d[0] = c[0]; d[1] = c[1]; d[2] = e[0]; d[3] = e[1];
+}
+
 // Eight consecutive elements of X from memory or LDS (16-byte pieces) as bf16 parts.
 template <typename TX> struct XParts { static constexpr int n = sizeof(TX) == 4 ? 3 : 1; };
 __device__ inline void x_parts(const __bf16 *p0, const __bf16 *, bf16x8 (&p)[1]) { p[0] = *(const bf16x8 *)p0; }

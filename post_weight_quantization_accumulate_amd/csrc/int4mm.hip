@@ -8,6 +8,8 @@
 // more are summed apart and scaled once (int4_tile.hip for many rows,
 // int4_skinny.hip for few); smaller groups are the kernel of this file.
 #include "gq.h"
+
+#include "gemv.h"
 #include "int4mm.h"
 
 namespace gq {
@@ -106,10 +108,15 @@ hipError_t launch_int4(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s)
         if (x_bf16) return nf4 ? launch_small_group<__bf16, true>(a, s) : launch_small_group<__bf16, false>(a, s);
         return nf4 ? launch_small_group<float, true>(a, s) : launch_small_group<float, false>(a, s);
     }
-    // the tile kernel's 32-bit offsets within a tile: 128 rows of X, 256 of codes
-    const bool fits = a.ldx <= 1 << 22 && a.K <= 1 << 22;
     const int64_t rows = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
-    if (rows > 64 && fits) return launch_int4_tile(a, x_bf16, nf4, s);
+    GemvArgs v{};
+    v.Y = a.Y; v.X = a.X; v.codes = a.codes; v.scales = a.scales; v.offsets = a.offsets;
+    v.M = a.M; v.ldx = a.ldx; v.ldy = a.ldy; v.E = a.E;
+    v.N = a.N; v.K = a.K; v.G = a.G;
+    v.y_bf16 = a.y_bf16; v.x_bf16 = x_bf16;
+    const int kind = nf4 ? GEMV_NF4 : GEMV_INT4;
+    if (rows <= kGemvMaxRows && gemv_ok(v, kind, (int)rows)) return launch_gemv(v, kind, (int)rows, s);
+    if (rows > 64) return launch_int4_tile(a, x_bf16, nf4, s);
     return launch_int4_skinny(a, x_bf16, nf4, s);
 }
 
@@ -133,7 +140,9 @@ int int4_run(void *Y, int y_dtype, int64_t ldy, const void *X, int x_dtype, int6
     if (group < 1 || group > 128 || (group & (group - 1)) || K % group)
         return set_error(GQ_ERR_INVALID_ARG, "group must be a power of two <= 128 that divides K");
     if (ldx < K || ldy < N) return set_error(GQ_ERR_INVALID_ARG, "a row stride is below the row's length");
-    if (M > INT32_MAX || N > (1 << 24) || K > (1 << 24)) return set_error(GQ_ERR_INVALID_ARG, "size too large");
+    // the kernels' offsets within a tile (128 rows of X, 256 of codes and scales) have 32 bits
+    if (M > INT32_MAX || N > (1 << 24) || K > (1 << 22) || ldx > (1 << 22))
+        return set_error(GQ_ERR_INVALID_ARG, "size too large");
     if (M == 0) return set_error(GQ_OK, "");
     if (!Y || !X || !codes || !scales) return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
     I4Args a{};

@@ -143,6 +143,22 @@ __device__ inline unsigned lds_offset(const void *p)
     return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
+// Loads through a buffer descriptor: `bytes` from p, anything past them reads as
+// zero without touching memory, so a load can be left out by its offset, with no
+// branch around it (a branch makes the compiler wait for every load in flight).
+// Dword aligned.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr unsigned kNoLoad = 0xFFFFFFF0u;
+__device__ inline Buffer make_buffer(const void *p, unsigned bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, bytes, 0x00027000);   // raw, 32-bit data
+}
+__device__ inline u32x4 buffer_load16(Buffer b, unsigned off)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+}
+__device__ inline unsigned buffer_load4(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0); }
+
 // 16 bytes from p, of which only the first n are the caller's (the rest zero);
 // p may be unaligned.
 __device__ inline u32x4 load16(const uint8_t *p, int n)
