@@ -11,57 +11,155 @@ namespace {
 constexpr int kBlock = 128;
 constexpr float kE4m3Max = 448.0f;
 
-__device__ inline float load_f(const float *p) { return *p; }
-__device__ inline float load_f(const __bf16 *p) { return (float)*p; }
-
-// The code of x under scale s: e4m3 of x / s (IEEE division, round to nearest
-// even, clamped to +-448, NaN kept); 0 where the scale is 0.
-__device__ inline unsigned fp8_code2(float x0, float x1, float s)
+// Eight consecutive elements of a row from column c, zero past K.  VEC: all or
+// none of them are within K and they start on 16 bytes.
+template <bool VEC> __device__ inline void load8(const __bf16 *row, int64_t c, int64_t K, float (&v)[8])
 {
-    float q0 = x0 / s, q1 = x1 / s;
-    q0 = q0 != q0 ? q0 : fminf(fmaxf(q0, -kE4m3Max), kE4m3Max);
-    q1 = q1 != q1 ? q1 : fminf(fmaxf(q1, -kE4m3Max), kE4m3Max);
-    return s == 0.0f ? 0u : (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(q0, q1, 0, false) & 0xFFFFu;
+    bf16x8 x{};
+    if constexpr (VEC) {
+        if (c < K) x = *(const bf16x8 *)(row + c);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (c + t < K) x[t] = row[c + t];
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = (float)x[t];
+}
+template <bool VEC> __device__ inline void load8(const float *row, int64_t c, int64_t K, float (&v)[8])
+{
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = 0.0f;
+    if constexpr (VEC) {
+        if (c < K) {
+            const f32x4 a = *(const f32x4 *)(row + c), b = *(const f32x4 *)(row + c + 4);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) { v[t] = a[t]; v[t + 4] = b[t]; }
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (c + t < K) v[t] = row[c + t];
+    }
 }
 
-// One block of BR x 128 elements per workgroup: its largest magnitude (as bits,
-// so that a NaN is the largest of all), the scale, the codes.
-template <typename TX, int BR>
-__global__ __launch_bounds__(256) void fp8_pack_kernel(uint8_t *codes, float *scales, const TX *X, int64_t ldx,
-                                                       int64_t rows, int64_t K, int64_t kb)
+// The largest magnitude of eight values as bits: a NaN is the largest of all.
+__device__ inline unsigned absmax8(const float (&v)[8])
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) m = max(m, __float_as_uint(v[t]) & 0x7FFFFFFFu);
+    return m;
+}
+template <int N> __device__ inline unsigned max_ror(unsigned v)
+{
+    return max(v, (unsigned)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, true));
+}
+// The largest over each group of 16 lanes.
+__device__ inline unsigned max16(unsigned v) { return max_ror<1>(max_ror<2>(max_ror<4>(max_ror<8>(v)))); }
+
+// Codes of eight values under scale s, stored at p (8-byte aligned when VEC): e4m3
+// of v / s (IEEE division, round to nearest even, clamped to +-448, NaN kept);
+// 0 where the scale is 0.
+template <bool VEC> __device__ inline void store8(uint8_t *row, int64_t c, int64_t K, const float (&v)[8], float s)
+{
+    unsigned w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float q[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float d = v[4 * h + t] / s;
+            q[t] = d != d ? d : fminf(fmaxf(d, -kE4m3Max), kE4m3Max);
+        }
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+        w[h] = s == 0.0f ? 0u : (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+    }
+    if constexpr (VEC) {
+        if (c < K) *(uint2 *)(row + c) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (c + t < K) row[c + t] = (uint8_t)(w[t / 4] >> (8 * (t & 3)));
+    }
+}
+
+// Blocks of one row: 16 lanes of 8 elements each, so a wave reads and writes four
+// neighbouring blocks of a row as one run, and a block's maximum is four steps
+// within its lanes.  Two units of work per lane keep two loads in flight.
+template <typename TX, bool VEC>
+__global__ __launch_bounds__(256) void fp8_pack_rows_kernel(uint8_t *codes, float *scales, const TX *X, int64_t ldx,
+                                                            int64_t units, int64_t K, int64_t kb)
+{
+    constexpr int U = 2;
+    const int g = threadIdx.x >> 4, l = threadIdx.x & 15;
+    float v[U][8];
+    int64_t row[U], c[U];
+    bool in[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t b = (int64_t)blockIdx.x * (16 * U) + 16 * u + g;
+        in[u] = b < units;
+        row[u] = in[u] ? b / kb : 0;
+        c[u] = in[u] ? (b - row[u] * kb) * kBlock + 8 * l : K;
+        load8<VEC>(X + row[u] * ldx, c[u], K, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float s = __uint_as_float(max16(absmax8(v[u]))) / kE4m3Max;
+        if (in[u] && l == 0) scales[row[u] * kb + c[u] / kBlock] = s;
+        store8<VEC>(codes + row[u] * K, c[u], K, v[u], s);
+    }
+}
+
+// Blocks of 128 rows: one per workgroup, held in registers (64 values per thread)
+// between the maximum and the codes, so the matrix is read once.
+template <typename TX, bool VEC>
+__global__ __launch_bounds__(256) void fp8_pack_block_kernel(uint8_t *codes, float *scales, const TX *X, int64_t ldx,
+                                                             int64_t rows, int64_t K, int64_t kb)
 {
     __shared__ unsigned red[4];
     const int64_t rb = grid_row(), cb = blockIdx.x;
-    if (rb * BR >= rows) return;
-    const int tid = threadIdx.x;
+    if (rb * kBlock >= rows) return;
+    const int64_t c = cb * kBlock + 8 * (threadIdx.x & 15), r0 = rb * kBlock + (threadIdx.x >> 4);
+    float v[8][8];
     unsigned mx = 0;
-    for (int i = tid; i < BR * kBlock; i += 256) {
-        const int64_t r = rb * BR + i / kBlock, c = cb * kBlock + i % kBlock;
-        if (r < rows && c < K) mx = max(mx, __float_as_uint(load_f(X + r * ldx + c)) & 0x7FFFFFFFu);
-    }
-    for (int d = 32; d; d >>= 1) mx = max(mx, (unsigned)__shfl_xor((int)mx, d));
-    if ((tid & 63) == 0) red[tid >> 6] = mx;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) load8<VEC>(X + min(r0 + 16 * u, rows - 1) * ldx, c, K, v[u]);   // a repeated row changes no maximum
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mx = max(mx, absmax8(v[u]));
+    mx = max16(mx);
+    mx = max(mx, (unsigned)__shfl_xor((int)mx, 16));
+    mx = max(mx, (unsigned)__shfl_xor((int)mx, 32));
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
     __syncthreads();
-    mx = max(max(red[0], red[1]), max(red[2], red[3]));
-    const float s = __uint_as_float(mx) / kE4m3Max;
-    if (tid == 0) scales[rb * kb + cb] = s;
-    for (int i = tid; i < BR * kBlock; i += 256) {
-        const int64_t r = rb * BR + i / kBlock, c = cb * kBlock + i % kBlock;
-        if (r < rows && c < K) codes[r * K + c] = (uint8_t)fp8_code2(load_f(X + r * ldx + c), 0.0f, s);
-    }
+    const float s = __uint_as_float(max(max(red[0], red[1]), max(red[2], red[3]))) / kE4m3Max;
+    if (threadIdx.x == 0) scales[rb * kb + cb] = s;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        if (r0 + 16 * u < rows) store8<VEC>(codes + (r0 + 16 * u) * K, c, K, v[u], s);
 }
 
-template <typename TX>
+template <typename TX, bool VEC>
 hipError_t launch_pack(uint8_t *codes, float *scales, const TX *X, int64_t ldx, int64_t rows, int64_t K,
                        int64_t block_rows, hipStream_t s)
 {
     const int64_t kb = (K + kBlock - 1) / kBlock;
-    const dim3 grid = tile_grid(kb, (rows + block_rows - 1) / block_rows);
     if (block_rows == 1)
-        hipLaunchKernelGGL((fp8_pack_kernel<TX, 1>), grid, dim3(256), 0, s, codes, scales, X, ldx, rows, K, kb);
+        hipLaunchKernelGGL((fp8_pack_rows_kernel<TX, VEC>), dim3((unsigned)((rows * kb + 31) / 32)), dim3(256), 0, s,
+                           codes, scales, X, ldx, rows * kb, K, kb);
     else
-        hipLaunchKernelGGL((fp8_pack_kernel<TX, 128>), grid, dim3(256), 0, s, codes, scales, X, ldx, rows, K, kb);
+        hipLaunchKernelGGL((fp8_pack_block_kernel<TX, VEC>), tile_grid(kb, (rows + kBlock - 1) / kBlock), dim3(256), 0, s,
+                           codes, scales, X, ldx, rows, K, kb);
     return hipGetLastError();
+}
+template <typename TX>
+hipError_t launch_pack(uint8_t *codes, float *scales, const TX *X, int64_t ldx, int64_t rows, int64_t K,
+                       int64_t block_rows, hipStream_t s)
+{
+    const bool vec = K % 8 == 0 && ((uintptr_t)X & 15) == 0 && (ldx * sizeof(TX)) % 16 == 0 && ((uintptr_t)codes & 7) == 0;
+    return vec ? launch_pack<TX, true>(codes, scales, X, ldx, rows, K, block_rows, s)
+               : launch_pack<TX, false>(codes, scales, X, ldx, rows, K, block_rows, s);
 }
 
 struct F8Args {
@@ -363,7 +461,8 @@ int fp8_quantize(uint8_t *codes, float *scales, const void *X, int x_dtype, int6
     if (rows < 0 || K < 1 || ldx < K) return set_error(GQ_ERR_INVALID_ARG, "bad sizes");
     if (rows == 0) return set_error(GQ_OK, "");
     if (!codes || !scales || !X) return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
-    if (K > (1 << 24) || rows > INT32_MAX) return set_error(GQ_ERR_INVALID_ARG, "size too large");
+    if (K > (1 << 24) || rows > INT32_MAX || rows * ((K + kBlock - 1) / kBlock) >= (int64_t)1 << 28)
+        return set_error(GQ_ERR_INVALID_ARG, "size too large");
     const hipError_t e = x_dtype == GQ_F32
                              ? launch_pack(codes, scales, (const float *)X, ldx, rows, K, block_rows, stream)
                              : launch_pack(codes, scales, (const __bf16 *)X, ldx, rows, K, block_rows, stream);
