@@ -487,7 +487,8 @@ int fp8_matmul_experts(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, con
  *   order    n ints: the slot of each row; -1 from offsets[E] on.
  *   pos      n ints: the row of each slot; -1 for a dropped one.
  *   ids      n choices of id_bytes (4 or 8) bytes each, signed.
- *   ws       experts_sort_workspace_size(n, E) bytes.
+ *   ws       experts_sort_workspace_size(n, E) bytes (0, and ws may be NULL, for
+ *            up to 4096 slots), 4-byte aligned.
  */
 size_t experts_sort_workspace_size(int64_t n, int64_t E);
 int experts_sort(int32_t *offsets, int32_t *order, int32_t *pos, const void *ids, int id_bytes, int64_t n, int64_t E,

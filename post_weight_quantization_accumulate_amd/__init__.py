@@ -580,10 +580,11 @@ def experts_sort_workspace_size(n: int, E: int) -> int:
     return int(lib().experts_sort_workspace_size(n, E))
 
 
-def experts_sort(offsets, order, pos, ids, ws) -> None:
+def experts_sort(offsets, order, pos, ids, ws=None) -> None:
     """A router's choices (ids: T x k, int32 or int64) ordered by expert, E =
     offsets.numel() - 1 experts: offsets (E + 1), order (T k, each row's slot) and
-    pos (like ids, each slot's row or -1), all int32."""
+    pos (like ids, each slot's row or -1), all int32.  ws: experts_sort_workspace_size
+    bytes, None where that is 0."""
     n, E = ids.numel(), offsets.numel() - 1
     if ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be int32 or int64")
@@ -591,9 +592,10 @@ def experts_sort(offsets, order, pos, ids, ws) -> None:
     _shape(offsets, "offsets", torch.int32, (E + 1,))
     _shape(order, "order", torch.int32, (n,))
     _shape(pos, "pos", torch.int32, tuple(ids.shape))
-    _shape(ws, "ws", torch.uint8, (ws.numel(),))
+    if ws is not None:
+        _shape(ws, "ws", torch.uint8, (ws.numel(),))
     _launch("experts_sort", ids, (offsets, order, pos, ws), offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
-            ids.data_ptr(), ids.element_size(), n, E, ws.data_ptr(), ws.numel())
+            ids.data_ptr(), ids.element_size(), n, E, *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())))
 
 
 def _pos(pos, T):

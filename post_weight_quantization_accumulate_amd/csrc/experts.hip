@@ -13,15 +13,18 @@ namespace gq {
 namespace {
 
 // ---------------------------------------------------------------- sort
-// A choice outside 0 .. E - 1 is dropped: it counts as expert E and its place
-// is past the last row.  kSortItems slots per workgroup.  The rank of a slot
-// among those of its expert is the number before it in its workgroup (by wave
-// ballots: the lanes of equal expert are the AND of the ballots of its bits)
-// plus the counts of the workgroups before.  No atomics: the order depends on
-// nothing but the ids.
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
+// A choice outside 0 .. E - 1 is dropped: it counts as expert E, whose places
+// come after the last row.  The rank of a slot among those of its expert is the
+// number before it in its chunk of 1024 slots (by wave ballots: the lanes of equal
+// expert are the AND of the ballots of its bits) plus the counts of the chunks
+// before.  Only whole-number counts are added by atomics, so the order depends on
+// nothing but the ids.  Up to kSortSmall slots one workgroup does it all, chunk
+// after chunk, in one launch; more take three: counts per chunk, prefix sums over
+// the chunks (a wave per expert), places.
+constexpr int kChunk = 1024;
+constexpr int kChunkWaves = kChunk / 64;
 constexpr int kMaxBuckets = GQ_MAX_EXPERTS + 1;
+constexpr int64_t kSortSmall = 4 * kChunk;
 
 template <typename TI> __device__ inline int bucket_of(const TI *ids, int64_t i, int E)
 {
@@ -41,22 +44,20 @@ __device__ inline unsigned long long same_bucket(int b, int bits, unsigned long 
     return m;
 }
 
-// Counts of each bucket among this workgroup's slots, wave by wave in
-// cnt[wave * (E + 1) + bucket] (LDS), and the rank of this thread's slot within
-// its wave.  On return cnt holds, for each wave, the number in the waves before.
-// Returns the rank within the workgroup; *total (per bucket) to tot.
-__device__ inline int rank_in_group(int b, bool in, int E, int bits, unsigned short *cnt, int *tot)
+// Rank of this thread's slot (if in) among those of bucket b in the workgroup's
+// chunk.  cnt: (E + 1) * waves counts in LDS; tot[bucket]: the chunk's counts.
+__device__ inline int rank_in_chunk(int b, bool in, int E, int bits, unsigned short *cnt, int *tot)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = E + 1;
-    for (int i = threadIdx.x; i < nb * kSortWaves; i += kSortThreads) cnt[i] = 0;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = E + 1, nt = blockDim.x, nw = nt >> 6;
+    for (int i = threadIdx.x; i < nb * nw; i += nt) cnt[i] = 0;
     __syncthreads();
     const unsigned long long same = same_bucket(b, bits, __ballot(in));
     const int rank = __popcll(same & ((1ull << lane) - 1));
     if (in && rank == 0) cnt[wave * nb + b] = (unsigned short)__popcll(same);
     __syncthreads();
-    for (int i = threadIdx.x; i < nb; i += kSortThreads) {
+    for (int i = threadIdx.x; i < nb; i += nt) {
         int s = 0;
-        for (int w = 0; w < kSortWaves; ++w) {
+        for (int w = 0; w < nw; ++w) {
             const int c = cnt[w * nb + i];
             cnt[w * nb + i] = (unsigned short)s;
             s += c;
@@ -67,63 +68,108 @@ __device__ inline int rank_in_group(int b, bool in, int E, int bits, unsigned sh
     return in ? rank + cnt[wave * nb + b] : 0;
 }
 
-// Workgroup w: hist[w (E + 1) + bucket] = its slots of each bucket.
-template <typename TI>
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int *hist, const TI *ids, int64_t n, int E)
+__device__ inline int wave_inclusive(int v)
 {
-    __shared__ int tot[kMaxBuckets];
-    for (int i = threadIdx.x; i <= E; i += kSortThreads) tot[i] = 0;
-    __syncthreads();
-    const int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
-    if (i < n) atomicAdd(&tot[bucket_of(ids, i, E)], 1);      // whole numbers: any order gives the same
-    __syncthreads();
-    for (int j = threadIdx.x; j <= E; j += kSortThreads) hist[(int64_t)blockIdx.x * (E + 1) + j] = tot[j];
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
 }
 
-// One workgroup: offsets (the exclusive sum of the buckets' totals), and each
-// workgroup's count of a bucket replaced by that bucket's first place in it.
-__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(int *hist, int *offsets, int nwg, int E)
+// base[i] = v[0] + .. + v[i - 1] for i < n, by the first wave; v may be base.
+// Ends with the workgroup synchronised.
+__device__ inline void exclusive_scan(int *base, const int *v, int n)
 {
-    __shared__ int base[kMaxBuckets];
-    const int nb = E + 1;
-    for (int b = threadIdx.x; b < nb; b += kSortThreads) {
-        int s = 0;
-        for (int w = 0; w < nwg; ++w) s += hist[(int64_t)w * nb + b];
-        base[b] = s;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int s = 0;
-        for (int b = 0; b < nb; ++b) {
-            const int c = base[b];
-            base[b] = s;
-            offsets[b] = s;                       // offsets[E] = the rows kept
-            s += c;
+    if (threadIdx.x < 64) {
+        int carry = 0;
+        for (int i0 = 0; i0 < n; i0 += 64) {
+            const int i = i0 + (int)threadIdx.x;
+            const int c = i < n ? v[i] : 0;
+            const int inc = wave_inclusive(c);
+            if (i < n) base[i] = carry + inc - c;
+            carry += __shfl(inc, 63);
         }
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < nb; b += kSortThreads) {
-        int s = base[b];
-        for (int w = 0; w < nwg; ++w) {
-            const int c = hist[(int64_t)w * nb + b];
-            hist[(int64_t)w * nb + b] = s;
-            s += c;
-        }
-    }
 }
 
 template <typename TI>
-__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(int *order, int *pos, const int *hist, const TI *ids,
-                                                                  int64_t n, int E, int bits)
+__global__ __launch_bounds__(kChunk) void sort_small_kernel(int *offsets, int *order, int *pos, const TI *ids, int n,
+                                                            int E, int bits)
 {
     extern __shared__ unsigned short cnt[];
+    __shared__ int base[kMaxBuckets], tot[kMaxBuckets];
+    const int nb = E + 1, nt = blockDim.x;
+    for (int b = threadIdx.x; b < nb; b += nt) tot[b] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += nt) atomicAdd(&tot[bucket_of(ids, i, E)], 1);
+    __syncthreads();
+    exclusive_scan(base, tot, nb);
+    for (int b = threadIdx.x; b < nb; b += nt) offsets[b] = base[b];
+    for (int i0 = 0; i0 < n; i0 += nt) {
+        const int i = i0 + (int)threadIdx.x;
+        const bool in = i < n;
+        const int b = in ? bucket_of(ids, i, E) : E;
+        const int rank = rank_in_chunk(b, in, E, bits, cnt, tot);
+        if (in) {
+            const int p = base[b] + rank;
+            order[p] = b < E ? i : -1;
+            pos[i] = b < E ? p : -1;
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < nb; j += nt) base[j] += tot[j];
+        // the next chunk's first barrier orders this before its reads
+    }
+}
+
+// hist[chunk][bucket] = the chunk's slots of each bucket.
+template <typename TI>
+__global__ __launch_bounds__(kChunk) void sort_count_kernel(int *hist, const TI *ids, int64_t n, int E)
+{
     __shared__ int tot[kMaxBuckets];
-    const int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
+    for (int b = threadIdx.x; b <= E; b += kChunk) tot[b] = 0;
+    __syncthreads();
+    const int64_t i = (int64_t)blockIdx.x * kChunk + threadIdx.x;
+    if (i < n) atomicAdd(&tot[bucket_of(ids, i, E)], 1);
+    __syncthreads();
+    for (int b = threadIdx.x; b <= E; b += kChunk) hist[(int64_t)blockIdx.x * (E + 1) + b] = tot[b];
+}
+
+// One wave per bucket: its counts become the number in the chunks before, its
+// total goes behind the last chunk (hist[chunks][bucket]).
+__global__ __launch_bounds__(64) void sort_prefix_kernel(int *hist, int chunks, int E)
+{
+    const int b = blockIdx.x, nb = E + 1;
+    int carry = 0;
+    for (int w0 = 0; w0 < chunks; w0 += 64) {
+        const int w = w0 + (int)threadIdx.x;
+        const int c = w < chunks ? hist[(int64_t)w * nb + b] : 0;
+        const int inc = wave_inclusive(c);
+        if (w < chunks) hist[(int64_t)w * nb + b] = carry + inc - c;
+        carry += __shfl(inc, 63);
+    }
+    if (threadIdx.x == 0) hist[(int64_t)chunks * nb + b] = carry;
+}
+
+template <typename TI>
+__global__ __launch_bounds__(kChunk) void sort_place_kernel(int *offsets, int *order, int *pos, const int *hist,
+                                                            const TI *ids, int64_t n, int E, int bits)
+{
+    extern __shared__ unsigned short cnt[];
+    __shared__ int base[kMaxBuckets], tot[kMaxBuckets];
+    const int nb = E + 1;
+    exclusive_scan(base, hist + (int64_t)gridDim.x * nb, nb);
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < nb; b += kChunk) offsets[b] = base[b];
+    const int64_t i = (int64_t)blockIdx.x * kChunk + threadIdx.x;
     const bool in = i < n;
     const int b = in ? bucket_of(ids, i, E) : E;
-    const int rank = rank_in_group(b, in, E, bits, cnt, tot);
+    const int rank = rank_in_chunk(b, in, E, bits, cnt, tot);
     if (!in) return;
-    const int p = hist[(int64_t)blockIdx.x * (E + 1) + b] + rank;
+    const int p = base[b] + hist[(int64_t)blockIdx.x * nb + b] + rank;
     order[p] = b < E ? (int)i : -1;
     pos[i] = b < E ? p : -1;
 }
@@ -131,14 +177,19 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(int *order, in
 template <typename TI>
 hipError_t launch_sort(int *offsets, int *order, int *pos, const TI *ids, int64_t n, int E, int *hist, hipStream_t s)
 {
-    const int nwg = (int)((n + kSortThreads - 1) / kSortThreads);
+    const int chunks = (int)((n + kChunk - 1) / kChunk);
     int bits = 0;
     while ((1 << bits) < E + 1) ++bits;
-    if (n) hipLaunchKernelGGL(sort_count_kernel<TI>, dim3(nwg), dim3(kSortThreads), 0, s, hist, ids, n, E);
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kSortThreads), 0, s, hist, offsets, nwg, E);
-    if (n)
-        hipLaunchKernelGGL(sort_place_kernel<TI>, dim3(nwg), dim3(kSortThreads),
-                           sizeof(unsigned short) * kSortWaves * (E + 1), s, order, pos, hist, ids, n, E, bits);
+    if (n <= kSortSmall) {
+        const int nt = n >= kChunk ? kChunk : n > 64 ? (int)((n + 63) / 64) * 64 : 64;
+        hipLaunchKernelGGL(sort_small_kernel<TI>, dim3(1), dim3(nt), sizeof(unsigned short) * (nt / 64) * (E + 1), s,
+                           offsets, order, pos, ids, (int)n, E, bits);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(sort_count_kernel<TI>, dim3(chunks), dim3(kChunk), 0, s, hist, ids, n, E);
+    hipLaunchKernelGGL(sort_prefix_kernel, dim3(E + 1), dim3(64), 0, s, hist, chunks, E);
+    hipLaunchKernelGGL(sort_place_kernel<TI>, dim3(chunks), dim3(kChunk),
+                       sizeof(unsigned short) * kChunkWaves * (E + 1), s, offsets, order, pos, hist, ids, n, E, bits);
     return hipGetLastError();
 }
 
@@ -302,7 +353,7 @@ extern "C" {
 size_t experts_sort_workspace_size(int64_t n, int64_t E)
 {
     if (n < 0 || n > INT32_MAX || E < 1 || E > GQ_MAX_EXPERTS) return 0;
-    return (size_t)((n + kSortThreads - 1) / kSortThreads) * (size_t)(E + 1) * sizeof(int);
+    return n <= kSortSmall ? 0 : (size_t)((n + kChunk - 1) / kChunk + 1) * (size_t)(E + 1) * sizeof(int);
 }
 
 int experts_sort(int32_t *offsets, int32_t *order, int32_t *pos, const void *ids, int id_bytes, int64_t n, int64_t E,
@@ -311,9 +362,10 @@ int experts_sort(int32_t *offsets, int32_t *order, int32_t *pos, const void *ids
     if (id_bytes != 4 && id_bytes != 8) return set_error(GQ_ERR_INVALID_ARG, "ids must be of 4 or 8 bytes");
     if (n < 0 || n > INT32_MAX) return set_error(GQ_ERR_INVALID_ARG, "bad number of slots");
     if (E < 1 || E > GQ_MAX_EXPERTS) return set_error(GQ_ERR_INVALID_ARG, "E must be 1 .. GQ_MAX_EXPERTS");
-    if (!offsets || (n && (!order || !pos || !ids || !ws)))
-        return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
-    if (ws_bytes < experts_sort_workspace_size(n, E)) return set_error(GQ_ERR_INVALID_ARG, "workspace too small");
+    if (!offsets || (n && (!order || !pos || !ids))) return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
+    const size_t need = experts_sort_workspace_size(n, E);
+    if (need && !ws) return set_error(GQ_ERR_INVALID_ARG, "null workspace");
+    if (ws_bytes < need) return set_error(GQ_ERR_INVALID_ARG, "workspace too small");
     return done(id_bytes == 4
                     ? launch_sort(offsets, order, pos, (const int32_t *)ids, n, (int)E, (int *)ws, stream)
                     : launch_sort(offsets, order, pos, (const int64_t *)ids, n, (int)E, (int *)ws, stream));

@@ -47,7 +47,8 @@ def _sort_ref(ids, E):
 @pytest.mark.parametrize("dt", [torch.int32, torch.int64])
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (4, 8, 128), (7, 3, 5), (1000, 2, 64), (512, 2, 8), (128, 8, 1024),
                                    (1025, 1, 3), (5000, 8, 128), (0, 2, 4), (300, 7, 1023), (3000, 4, 2), (40000, 3, 60),
-                                   (129, 8, 16), (2047, 1, 256)])
+                                   (129, 8, 16), (2047, 1, 256), (4096, 1, 1024), (4097, 1, 1024),
+                                   (70000, 1, 512)])
 def test_sort(gq, T, k, E, dt):
     rng = np.random.default_rng(T + k + E)
     ids = torch.from_numpy(rng.integers(-1, E + 1, (T, k))).to(dt)       # some of them dropped, on both sides
