@@ -193,123 +193,184 @@ hipError_t launch_sort(int *offsets, int *order, int *pos, const TI *ids, int64_
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------- gather
-constexpr int kRowThreads = 256;
+// ---------------------------------------------------------------- rows
+// A thread takes V consecutive columns of a row: 16 bytes, whatever the row's
+// alignment (memory takes unaligned accesses), or one element where a row is
+// shorter than that.  The last thread of a row moves back to end with it, and
+// repeats what its neighbour does.  A token's rows are taken KR at a time with
+// all their loads in flight: a slot without a row reads zeros from a line of its
+// own rather than branch, since a branch between loads makes the compiler wait
+// for those before it (8192 x 8 rows of 5120 bf16 combined with such branches:
+// 210 us).
+constexpr int kMaxRowThreads = 512;
+__device__ __attribute__((aligned(16))) const unsigned kZeros[4] = {0, 0, 0, 0};
 
-// One token per workgroup: its row read once and written to its k places.
-template <typename T, int V>
-__global__ __launch_bounds__(kRowThreads) void gather_kernel(T *Xs, int64_t lds, const T *X, int64_t ldx, const int *pos,
-                                                             int64_t rows, int64_t Tn, int k, int64_t D)
+template <typename T, int V> struct Vec {
+    T v[V];
+};
+template <typename T, int V> __device__ inline Vec<T, V> load_vec(const T *p)
 {
-    typedef T vec __attribute__((ext_vector_type(V)));
-    const int64_t t = grid_row();
-    if (t >= Tn) return;
-    const T *x = X + t * ldx;
-    for (int64_t c = threadIdx.x * V; c < D; c += kRowThreads * V) {
-        const vec v = *(const vec *)(x + c);
-        for (int j = 0; j < k; ++j) {
-            const int64_t p = pos[t * k + j];
-            if (p >= 0 && p < rows) *(vec *)(Xs + p * lds + c) = v;
-        }
+    Vec<T, V> r;
+    __builtin_memcpy(&r, p, sizeof r);
+    return r;
+}
+template <typename T, int V> __device__ inline void store_vec(T *p, const Vec<T, V> &r) { __builtin_memcpy(p, &r, sizeof r); }
+
+// Row of slot t k + j, or -1 (past k, dropped, or outside the rows).
+__device__ inline int64_t row_of(const int *pos, int64_t t, int j, int k, int64_t rows)
+{
+    const int p = pos[t * k + min(j, k - 1)];
+    return j < k && p >= 0 && p < rows ? p : -1;
+}
+template <typename T, int V> __device__ inline Vec<T, V> load_row(const T *Y, int64_t ldy, int64_t p, int64_t c)
+{
+    return load_vec<T, V>(p >= 0 ? Y + p * ldy + c : (const T *)kZeros);
+}
+
+// Each token's row read once and written to its places.
+template <typename T, int V, int KR>
+__global__ __launch_bounds__(kMaxRowThreads) void gather_kernel(T *Xs, int64_t lds, const T *X, int64_t ldx,
+                                                                const int *pos, int64_t rows, int64_t Tn, int k, int64_t D)
+{
+    const int64_t t = grid_row(), c0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V, c = min(c0, D - V);
+    if (t >= Tn || c0 >= D) return;
+    const Vec<T, V> x = load_vec<T, V>(X + t * ldx + c);
+    for (int j0 = 0; j0 < k; j0 += KR) {
+        int64_t p[KR];
+#pragma unroll
+        for (int j = 0; j < KR; ++j) p[j] = row_of(pos, t, j0 + j, k, rows);
+#pragma unroll
+        for (int j = 0; j < KR; ++j)
+            if (p[j] >= 0) store_vec(Xs + p[j] * lds + c, x);
     }
 }
 
-// ---------------------------------------------------------------- combine
-template <typename T, int V>
-__global__ __launch_bounds__(kRowThreads) void combine_kernel(T *out, int64_t ldo, const T *Y, int64_t ldy,
-                                                              const int *pos, const float *w, int64_t rows,
-                                                              int64_t Tn, int k, int64_t D)
+template <typename T, int V, int KR>
+__global__ __launch_bounds__(kMaxRowThreads) void combine_kernel(T *out, int64_t ldo, const T *Y, int64_t ldy,
+                                                                 const int *pos, const float *w, int64_t rows,
+                                                                 int64_t Tn, int k, int64_t D)
 {
-    typedef T vec __attribute__((ext_vector_type(V)));
-    const int64_t t = grid_row();
-    if (t >= Tn) return;
-    for (int64_t c = threadIdx.x * V; c < D; c += kRowThreads * V) {
-        float acc[V] = {};
-        for (int j = 0; j < k; ++j) {
-            const int64_t p = pos[t * k + j];
-            if (p < 0 || p >= rows) continue;
-            const float wt = w ? w[t * k + j] : 1.0f;
-            const vec v = *(const vec *)(Y + p * ldy + c);
+    const int64_t t = grid_row(), c0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V, c = min(c0, D - V);
+    if (t >= Tn || c0 >= D) return;
+    float acc[V] = {};
+    for (int j0 = 0; j0 < k; j0 += KR) {
+        Vec<T, V> y[KR];
+        float wt[KR];
 #pragma unroll
-            for (int u = 0; u < V; ++u) acc[u] = fmaf(wt, (float)v[u], acc[u]);
+        for (int j = 0; j < KR; ++j) {
+            const int64_t p = row_of(pos, t, j0 + j, k, rows);
+            wt[j] = p < 0 ? 0.0f : w ? w[t * k + j0 + j] : 1.0f;
+            y[j] = load_row<T, V>(Y, ldy, p, c);
         }
-        vec o;
 #pragma unroll
-        for (int u = 0; u < V; ++u) o[u] = (T)acc[u];
-        *(vec *)(out + t * ldo + c) = o;
+        for (int j = 0; j < KR; ++j)
+#pragma unroll
+            for (int u = 0; u < V; ++u) acc[u] = fmaf(wt[j], (float)y[j].v[u], acc[u]);
     }
+    Vec<T, V> o;
+#pragma unroll
+    for (int u = 0; u < V; ++u) o.v[u] = (T)acc[u];
+    store_vec(out + t * ldo + c, o);
 }
 
-// One token per workgroup: for each of its rows, dY = w dout and dw = <dout, Y>.
-template <typename T, int V>
-__global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(T *dY, int64_t lddy, float *dw, const T *dout,
-                                                                       int64_t ldo, const T *Y, int64_t ldy,
-                                                                       const int *pos, const float *w, int64_t rows,
-                                                                       int64_t Tn, int k, int64_t D)
+// One token per workgroup: dY = w dout for each of its rows, and the dot products
+// of dout with them, added over the workgroup in wave order.
+template <typename T, int V, int KR>
+__global__ __launch_bounds__(kMaxRowThreads) void combine_backward_kernel(T *dY, int64_t lddy, float *dw, const T *dout,
+                                                                          int64_t ldo, const T *Y, int64_t ldy,
+                                                                          const int *pos, const float *w, int64_t rows,
+                                                                          int64_t Tn, int k, int64_t D)
 {
-    typedef T vec __attribute__((ext_vector_type(V)));
-    __shared__ float red[kRowThreads / 64];
+    __shared__ float red[kMaxRowThreads / 64][KR];
     const int64_t t = grid_row();
     if (t >= Tn) return;
-    for (int j = 0; j < k; ++j) {
-        const int64_t p = pos[t * k + j];
-        const bool live = p >= 0 && p < rows;
-        const float wt = w[t * k + j];
-        float dot = 0.0f;
-        if (live)
-            for (int64_t c = threadIdx.x * V; c < D; c += kRowThreads * V) {
-                const vec g = *(const vec *)(dout + t * ldo + c);
-                const vec y = *(const vec *)(Y + p * ldy + c);
-                vec o;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    for (int j0 = 0; j0 < k; j0 += KR) {
+        int64_t p[KR];
+        float wt[KR], dot[KR] = {};
+#pragma unroll
+        for (int j = 0; j < KR; ++j) {
+            p[j] = row_of(pos, t, j0 + j, k, rows);
+            wt[j] = w[t * k + min(j0 + j, k - 1)];
+        }
+        for (int64_t c0 = threadIdx.x * V; c0 < D; c0 += blockDim.x * V) {
+            const int64_t c = min(c0, D - V);
+            Vec<T, V> g = load_vec<T, V>(dout + t * ldo + c), y[KR];
+#pragma unroll
+            for (int j = 0; j < KR; ++j) y[j] = load_row<T, V>(Y, ldy, p[j], c);
+#pragma unroll
+            for (int j = 0; j < KR; ++j) {
+                Vec<T, V> o;
 #pragma unroll
                 for (int u = 0; u < V; ++u) {
-                    dot = fmaf((float)g[u], (float)y[u], dot);
-                    o[u] = (T)(wt * (float)g[u]);
+                    // columns its neighbour has added are not added again
+                    dot[j] = fmaf(c + u >= c0 ? (float)g.v[u] : 0.0f, c + u >= c0 ? (float)y[j].v[u] : 0.0f, dot[j]);
+                    o.v[u] = (T)(wt[j] * (float)g.v[u]);
                 }
-                *(vec *)(dY + p * lddy + c) = o;
+                if (p[j] >= 0) store_vec(dY + p[j] * lddy + c, o);
             }
-        for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = dot;
+        }
+#pragma unroll
+        for (int j = 0; j < KR; ++j) {
+            float d = dot[j];
+#pragma unroll
+            for (int x = 32; x; x >>= 1) d += __shfl_xor(d, x);
+            if (lane == 0) red[wave][j] = d;
+        }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            float s = red[0];
-            for (int i = 1; i < kRowThreads / 64; ++i) s += red[i];
-            dw[t * k + j] = live ? s : 0.0f;
+        if (threadIdx.x < KR && j0 + (int)threadIdx.x < k) {
+            float s = red[0][threadIdx.x];
+            for (int i = 1; i < nw; ++i) s += red[i][threadIdx.x];
+            dw[t * k + j0 + threadIdx.x] = row_of(pos, t, j0 + threadIdx.x, k, rows) >= 0 ? s : 0.0f;
         }
         __syncthreads();
     }
 }
 
-// Whether rows of D elements of T at p, ld apart, can be taken in 16-byte pieces.
-template <typename T> bool vec_rows(const void *p, int64_t ld, int64_t D)
+// Threads for a row of D elements, V each: equal passes of at most kMaxRowThreads.
+int row_threads(int64_t D, int V, int64_t *passes)
 {
-    return ((uintptr_t)p & 15) == 0 && (ld * sizeof(T)) % 16 == 0 && (D * sizeof(T)) % 16 == 0;
+    const int64_t nv = (D + V - 1) / V;
+    const int64_t np = (nv + kMaxRowThreads - 1) / kMaxRowThreads;
+    const int nt = (int)(((nv + np - 1) / np + 63) / 64) * 64;
+    *passes = (nv + nt - 1) / nt;
+    return nt;
+}
+
+// Calls f<V, KR>: V for rows of D elements, KR for k choices.
+template <typename T, typename F> hipError_t by_shape(int64_t D, int k, F f)
+{
+    constexpr int V = 16 / sizeof(T);
+    if (D < V) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
+    if (k <= 2) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 2>{});
+    if (k <= 4) return f(std::integral_constant<int, V>{}, std::integral_constant<int, 4>{});
+    return f(std::integral_constant<int, V>{}, std::integral_constant<int, 8>{});
 }
 
 template <typename T>
 hipError_t launch_gather(T *Xs, int64_t lds, const T *X, int64_t ldx, const int *pos, int64_t rows, int64_t Tn, int k,
                          int64_t D, hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
-    const dim3 grid = tile_grid(1, Tn);
-    if (vec_rows<T>(Xs, lds, D) && vec_rows<T>(X, ldx, D))
-        hipLaunchKernelGGL((gather_kernel<T, V>), grid, dim3(kRowThreads), 0, s, Xs, lds, X, ldx, pos, rows, Tn, k, D);
-    else
-        hipLaunchKernelGGL((gather_kernel<T, 1>), grid, dim3(kRowThreads), 0, s, Xs, lds, X, ldx, pos, rows, Tn, k, D);
-    return hipGetLastError();
+    return by_shape<T>(D, k, [&](auto V, auto KR) {
+        int64_t passes;
+        const int nt = row_threads(D, V, &passes);
+        hipLaunchKernelGGL((gather_kernel<T, decltype(V)::value, decltype(KR)::value>), tile_grid(passes, Tn), dim3(nt), 0,
+                           s, Xs, lds, X, ldx, pos, rows, Tn, k, D);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>
 hipError_t launch_combine(T *out, int64_t ldo, const T *Y, int64_t ldy, const int *pos, const float *w, int64_t rows,
                           int64_t Tn, int k, int64_t D, hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
-    const dim3 grid = tile_grid(1, Tn);
-    if (vec_rows<T>(out, ldo, D) && vec_rows<T>(Y, ldy, D))
-        hipLaunchKernelGGL((combine_kernel<T, V>), grid, dim3(kRowThreads), 0, s, out, ldo, Y, ldy, pos, w, rows, Tn, k, D);
-    else
-        hipLaunchKernelGGL((combine_kernel<T, 1>), grid, dim3(kRowThreads), 0, s, out, ldo, Y, ldy, pos, w, rows, Tn, k, D);
-    return hipGetLastError();
+    return by_shape<T>(D, k, [&](auto V, auto KR) {
+        int64_t passes;
+        const int nt = row_threads(D, V, &passes);
+        hipLaunchKernelGGL((combine_kernel<T, decltype(V)::value, decltype(KR)::value>), tile_grid(passes, Tn), dim3(nt), 0,
+                           s, out, ldo, Y, ldy, pos, w, rows, Tn, k, D);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>
@@ -317,15 +378,13 @@ hipError_t launch_combine_backward(T *dY, int64_t lddy, float *dw, const T *dout
                                    const int *pos, const float *w, int64_t rows, int64_t Tn, int k, int64_t D,
                                    hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
-    const dim3 grid = tile_grid(1, Tn);
-    if (vec_rows<T>(dY, lddy, D) && vec_rows<T>(dout, ldo, D) && vec_rows<T>(Y, ldy, D))
-        hipLaunchKernelGGL((combine_backward_kernel<T, V>), grid, dim3(kRowThreads), 0, s, dY, lddy, dw, dout, ldo, Y,
-                           ldy, pos, w, rows, Tn, k, D);
-    else
-        hipLaunchKernelGGL((combine_backward_kernel<T, 1>), grid, dim3(kRowThreads), 0, s, dY, lddy, dw, dout, ldo, Y,
-                           ldy, pos, w, rows, Tn, k, D);
-    return hipGetLastError();
+    return by_shape<T>(D, k, [&](auto V, auto KR) {
+        int64_t passes;
+        const int nt = row_threads(D, V, &passes);
+        hipLaunchKernelGGL((combine_backward_kernel<T, decltype(V)::value, decltype(KR)::value>), tile_grid(1, Tn), dim3(nt),
+                           0, s, dY, lddy, dw, dout, ldo, Y, ldy, pos, w, rows, Tn, k, D);
+        return hipGetLastError();
+    });
 }
 
 int done(hipError_t e)
@@ -337,7 +396,7 @@ int done(hipError_t e)
 int check_rows(int dtype, int64_t T, int64_t k, int64_t rows, int64_t D)
 {
     if (dtype != GQ_F32 && dtype != GQ_BF16) return set_error(GQ_ERR_INVALID_ARG, "unknown dtype");
-    if (T < 0 || k < 1 || rows < 0 || D < 1) return set_error(GQ_ERR_INVALID_ARG, "bad sizes");
+    if (T < 0 || k < 1 || rows < 0 || D < 1 || D > (1 << 30)) return set_error(GQ_ERR_INVALID_ARG, "bad sizes");
     if (k > INT32_MAX || T > INT32_MAX / k || rows > INT32_MAX)
         return set_error(GQ_ERR_INVALID_ARG, "size too large");
     return GQ_OK;
