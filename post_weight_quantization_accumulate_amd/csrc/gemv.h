@@ -21,7 +21,7 @@ struct GemvArgs {
 };
 
 // Rows per tile above which the matrix cores win.
-constexpr int kGemvMaxRows = 4;
+constexpr int kGemvMaxRows = 2;
 // True if the kernel takes these sizes: rows of whole 16-byte pieces of 32 codes
 // (int4) or twice that (fp8), at most 16 waves to a row.
 bool gemv_ok(const GemvArgs &a, int kind, int rows);

@@ -1,4 +1,4 @@
-// gemv.hip -- pack products of one to four rows: a decoding step, where reading
+// gemv.hip -- pack products of one or two rows: a decoding step, where reading
 // the pack is the work.
 //
 // A lane owns 32 consecutive k for the whole call: their x stay in its registers
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(MAXT) void gemv_kernel(GemvArgs a)
 }
 
 // Waves of a workgroup that leave each the registers its x need.
-constexpr int max_waves(int mr) { return mr == 1 ? 16 : mr == 2 ? 10 : 8; }
+constexpr int max_waves(int mr) { return mr == 1 ? 16 : 10; }
 
 // Eight columns share each x; with fewer than two workgroups per CU of them
 // (N < 4096), four (1 x 1024 x 5120: 3.5 against 4.0 us; 1 x 10240 x 5120: 10.2
@@ -210,15 +210,14 @@ template <int KIND, typename TX, int MR> hipError_t launch_rows(const GemvArgs &
 template <int KIND, typename TX> hipError_t by_rows(const GemvArgs &a, int rows, hipStream_t s)
 {
     if (rows <= 1) return launch_rows<KIND, TX, 1>(a, s);
-    if (rows <= 2) return launch_rows<KIND, TX, 2>(a, s);
-    return launch_rows<KIND, TX, 4>(a, s);
+    return launch_rows<KIND, TX, 2>(a, s);
 }
 
 }  // namespace
 
 bool gemv_ok(const GemvArgs &a, int kind, int rows)
 {
-    return rows <= kGemvMaxRows && a.K % SEG == 0 && a.G >= SEG && (a.K / SEG + 63) / 64 <= max_waves(rows > 2 ? 4 : rows) &&
+    return rows <= kGemvMaxRows && a.K % SEG == 0 && a.G >= SEG && (a.K / SEG + 63) / 64 <= max_waves(rows) &&
            ((uintptr_t)a.codes & 15) == 0;
 }
 

@@ -126,6 +126,7 @@ __device__ inline void store_row(const I4Args &a, int64_t row, int n, float v)
 // Groups of 32 and more, any M, K, strides and alignment (int4_tile.hip).
 hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s);
 // The same for few rows (int4_skinny.hip).
-hipError_t launch_int4_skinny(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s);
+int64_t int4_skinny_cost(const I4Args &a, int *shape);
+hipError_t launch_int4_skinny(const I4Args &a, bool x_bf16, bool nf4, int shape, hipStream_t s);
 
 }  // namespace gq

@@ -130,7 +130,13 @@ __device__ inline void copy4_lds(const void *base, unsigned off, unsigned l)
 {
     asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(l) : "memory");
 }
-__device__ inline void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits until at most N of this wave's memory instructions are under way; they
+// end in order.
+template <int N = 0> __device__ inline void wait_copies()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 __device__ inline void publish()
 {
     wait_copies();
