@@ -185,69 +185,123 @@ __device__ inline bf16x8 bf16_of_fp8(unsigned w0, unsigned w1)
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Codes k .. k + 7 of a row as bf16, zero past K.
-template <bool VEC> __device__ inline bf16x8 load_f8(const uint8_t *row, int k, int K)
-{
-    unsigned w[2] = {0, 0};
-    if constexpr (VEC) {
-        if (k < K) {
-            const uint2 v = *(const uint2 *)(row + k);
-            w[0] = v.x;
-            w[1] = v.y;
-        }
-    } else {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-            if (k + t < K) w[t / 4] |= (unsigned)row[k + t] << (8 * (t & 3));
-    }
-    return bf16_of_fp8(w[0], w[1]);
-}
-
-constexpr int kWaves = 4;
-
+// ---------------------------------------------------------------- few rows
 // The fp8 matrix instructions add the 8 products of a lane's 8 consecutive k with
 // all but about 14 bits of the largest one cut off, and only the sums of 8 in
 // fp32 (seen by probing with powers of two); e4m3 codes fit bf16 exactly, and the
-// bf16 instructions keep fp32 throughout at half the rate.
+// bf16 instructions keep fp32 throughout at half the rate, which at few rows
+// costs nothing.
 //
-// One 16 x 16 tile of Y per workgroup, its blocks of 128 k dealt to four waves
-// and their sums added through LDS in wave order.
-template <typename TY, bool VEC> __global__ __launch_bounds__(64 * kWaves) void fp8_direct_kernel(F8Args a)
+// A workgroup takes 16 MT rows by 16 NT columns of Y; its waves take a range of K
+// each, one block of 128 k at a time, through rings of their own in LDS (see
+// ring), and add their sums in wave order.  A copy is 8 rows of 128 bytes, whole
+// cache lines; chunk c of row rho lies at position c ^ (rho & 7).
+template <typename TY, int MT, int NT, int W, int D>
+__global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(F8Args a)
 {
-    __shared__ float red[kWaves][256];
+    constexpr int C = 2 * (MT + NT), XB = 2048 * MT, SLOT = XB + 2048 * NT + 256 * MT;    // X, W, X's scales
+    static_assert(D * SLOT >= MT * NT * 1024, "the sums reuse the ring's space");
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     RowTile rt;
-    if (!row_tile(a.offsets, (int)a.E, a.M, 16, grid_row(), rt)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * 16;
-    const int n = min(n0 + r, a.N - 1);
-    const int64_t m = min(rt.r0 + r, rt.r1 - 1);
-    const uint8_t *x = a.Xq + m * a.K;
-    const uint8_t *w = a.Wq + (rt.e * a.N + n) * (int64_t)a.K;
-    const float *sx = a.xs + m * a.kb;
-    const float *sw = a.ws + (rt.e * ((a.N + kBlock - 1) / kBlock) + n0 / kBlock) * (int64_t)a.kb;
-    f32x4 acc{};
-    for (int b = wave; b < a.kb; b += kWaves) {
-        f32x4 part{};
+    if (!row_tile(a.offsets, (int)a.E, a.M, 16 * MT, grid_row(), rt)) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4, K = a.K, kb = a.kb;
+    const int n0 = blockIdx.x * 16 * NT;
+    const int mrows = (int)(rt.r1 - rt.r0);
+    const uint8_t *xbase = a.Xq + rt.r0 * K, *wbase = a.Wq + (rt.e * a.N + n0) * (int64_t)K;
+    const float *sxbase = a.xs + rt.r0 * kb;
+    const float *sw = a.ws + (rt.e * ((a.N + kBlock - 1) / kBlock) + n0 / kBlock) * (int64_t)kb;
+    const unsigned ch = 16u * ((lane & 7) ^ (lane >> 3));
+    unsigned off[C], so[MT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = b * kBlock + 32 * j + 8 * q;
-            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(load_f8<VEC>(w, k, a.K), load_f8<VEC>(x, k, a.K), part,
-                                                           0, 0, 0);
-        }
-        const float s = sx[b] * sw[b];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(s, part[i], acc[i]);
+    for (int i = 0; i < C; ++i) {
+        const int row = 8 * (i < 2 * MT ? i : i - 2 * MT) + (lane >> 3);
+        off[i] = (unsigned)min(row, (i < 2 * MT ? mrows : a.N - n0) - 1) * (unsigned)K;
     }
-    // acc[i]: column n0 + 4 q + i of row r
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][16 * r + 4 * q + i] = acc[i];
+    for (int i = 0; i < MT; ++i) so[i] = 4u * (unsigned)min(16 * i + r, mrows - 1) * (unsigned)kb;
+    uint8_t *mine = lds + wave * D * SLOT;
+    const unsigned mo = lds_offset(mine);
+    constexpr int LOADS = C + MT;
+    auto issue = [&](int b, int slot) {
+        const unsigned at = mo + slot * SLOT, k = min((unsigned)b * kBlock + ch, (unsigned)K - 16);   // past K: any of the row's own
+#pragma unroll
+        for (int i = 0; i < C; ++i) copy16_lds(i < 2 * MT ? xbase : wbase, off[i] + k, at + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) copy4_lds(sxbase + b, so[i], at + XB + 2048 * NT + 256 * i);
+    };
+    const int p0 = 128 * r + 16 * ((2 * q) ^ (r & 7)), p1 = 128 * r + 16 * ((2 * q + 1) ^ (r & 7));
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{};
+    auto use = [&](int b, int slot) {
+        const uint8_t *u = mine + slot * SLOT;
+        const float s_w = sw[b];
+        // the lane's k = 32 q .. + 31 of the block; K is a multiple of 16, so of its
+        // two halves each is within K or past it
+        const bool in0 = b * kBlock + 32 * q < K, in1 = b * kBlock + 32 * q + 16 < K;
+        u32x4 w[NT][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            w[j][0] = *(const u32x4 *)(u + XB + 2048 * j + p0);
+            w[j][1] = *(const u32x4 *)(u + XB + 2048 * j + p1);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            u32x4 x[2] = {*(const u32x4 *)(u + 2048 * i + p0), *(const u32x4 *)(u + 2048 * i + p1)};
+            x[0] = in0 ? x[0] : u32x4{};
+            x[1] = in1 ? x[1] : u32x4{};
+            const float s = *(const float *)(u + XB + 2048 * NT + 256 * i + 4 * r) * s_w;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                f32x4 part{};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const u32x4 wv = in0 && (h < 2 || in1) ? w[j][h >> 1] : u32x4{}, xv = x[h >> 1];
+                    const int t = 2 * (h & 1);
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_fp8(wv[t], wv[t + 1]), bf16_of_fp8(xv[t], xv[t + 1]),
+                                                                   part, 0, 0, 0);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(s, part[t], acc[i][j][t]);
+            }
+        }
+    };
+    const int per = (kb + W - 1) / W, b0 = wave * per;
+    ring<D, LOADS>(b0, min(b0 + per, kb), issue, use);
+    __syncthreads();                                     // every wave is past its ring
+    float *red = (float *)lds;
+    // acc[i][j][t]: column 16 j + 4 q + t of row 16 i + r
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *(f32x4 *)(red + wave * MT * NT * 256 + (16 * i + r) * 16 * NT + 16 * j + 4 * q) = acc[i][j];
     __syncthreads();
-    const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
-    float v = red[0][threadIdx.x];
+    for (int e = threadIdx.x; e < MT * NT * 256; e += 64 * W) {
+        float v = red[e];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) v += red[i][threadIdx.x];
-    if (rt.r0 + row < rt.r1 && n0 + col < a.N) store_y((TY *)a.Y + (rt.r0 + row) * a.ldy + n0 + col, v);
+        for (int w = 1; w < W; ++w) v += red[w * MT * NT * 256 + e];
+        const int64_t row = rt.r0 + e / (16 * NT);
+        const int n = n0 + e % (16 * NT);
+        if (row < rt.r1 && n < a.N) store_y((TY *)a.Y + row * a.ldy + n, v);
+    }
+}
+
+template <typename TY, int MT, int NT, int W, int D> hipError_t launch_skinny(const F8Args &a, hipStream_t s)
+{
+    constexpr size_t lds = (size_t)W * D * (2048 * (MT + NT) + 256 * MT);
+    static_assert(lds <= 160 * 1024, "LDS");
+    const auto kernel = fp8_skinny_kernel<TY, MT, NT, W, D>;
+    static const bool lds_ok =
+        hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
+    if (!lds_ok) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(kernel, tile_grid((a.N + 16 * NT - 1) / (16 * NT), row_tiles(a.offsets != nullptr, a.E, a.M, 16 * MT)),
+                       dim3(64 * W), lds, s, a);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- large tiles
@@ -417,12 +471,8 @@ template <typename TY> hipError_t launch_fp8(F8Args a, hipStream_t s)
     v.y_bf16 = sizeof(TY) == 2;
     const int64_t rows = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
     if (rows <= kGemvMaxRows && gemv_ok(v, GEMV_FP8, (int)rows)) return launch_gemv(v, GEMV_FP8, (int)rows, s);
-    if (a.M > 64 && a.K <= (1 << 22)) return dma ? launch_tile<TY, 2, 4, 8, 4, true>(a, s) : launch_tile<TY, 2, 4, 8, 4, false>(a, s);
-    const dim3 grid = tile_grid((a.N + 15) / 16, row_tiles(a.offsets != nullptr, a.E, a.M, 16));
-    const bool vec = a.K % 8 == 0 && ((uintptr_t)a.Xq & 7) == 0 && ((uintptr_t)a.Wq & 7) == 0;
-    if (vec) hipLaunchKernelGGL((fp8_direct_kernel<TY, true>), grid, dim3(64 * kWaves), 0, s, a);
-    else hipLaunchKernelGGL((fp8_direct_kernel<TY, false>), grid, dim3(64 * kWaves), 0, s, a);
-    return hipGetLastError();
+    if (dma && rows <= 64) return launch_skinny<TY, 1, 1, 4, 2>(a, s);
+    return dma ? launch_tile<TY, 2, 4, 8, 4, true>(a, s) : launch_tile<TY, 2, 4, 8, 4, false>(a, s);
 }
 
 }  // namespace
@@ -438,7 +488,8 @@ int fp8_run(void *Y, int y_dtype, int64_t ldy, const uint8_t *Xq, const float *x
     if (y_dtype != GQ_F32 && y_dtype != GQ_BF16) return set_error(GQ_ERR_INVALID_ARG, "unknown dtype");
     if (M < 0 || N < 1 || K < 1) return set_error(GQ_ERR_INVALID_ARG, "M must be >= 0, N and K >= 1");
     if (ldy < N) return set_error(GQ_ERR_INVALID_ARG, "a row stride is below the row's length");
-    if (M > INT32_MAX || N > (1 << 24) || K > (1 << 24)) return set_error(GQ_ERR_INVALID_ARG, "size too large");
+    // the kernels' offsets within a tile (256 rows of X and W) have 32 bits
+    if (M > INT32_MAX || N > (1 << 24) || K > (1 << 22)) return set_error(GQ_ERR_INVALID_ARG, "size too large");
     if (M == 0) return set_error(GQ_OK, "");
     if (!Y || !Xq || !xs || !Wq || !ws) return set_error(GQ_ERR_INVALID_ARG, "null required pointer");
     F8Args a{};

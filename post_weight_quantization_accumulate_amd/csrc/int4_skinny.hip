@@ -6,10 +6,10 @@
 // code is read once per 16 MT rows, X once per 16 NT columns (from L2), and what
 // bounds the kernel is how many cache lines its loads touch: a matrix operand
 // loaded as it is used takes 16 rows by 64 bytes, 16 half lines, so X goes
-// through LDS in whole lines instead (16 x 5120 x 10240: 20.7 -> MEASURE us), into
-// a part of the wave's own, with no barrier: the wave waits for its own copies.
-// A unit's loads are issued while the one before it is multiplied, in a loop
-// without branches: at a branch the compiler waits for every load in flight.
+// through LDS in whole lines instead (16 x 5120 x 10240: 20.7 -> 13.4 us).  Codes
+// and scales take the same way, so that the waits are the ring's own: the
+// compiler's, which does not know of the copies, would wait for those too.  The
+// ring is the wave's own part of LDS, with no barrier.
 #include "int4mm.h"
 
 namespace gq {
@@ -19,13 +19,14 @@ constexpr int KU = 128, NH = KU / 32;
 
 // XC: copies of X per unit, 1 KiB each; rows past them (there are none) hold
 // whatever was in LDS, in rows of Y that are not stored.
-template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC>
+template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC, int D>
 __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
 {
     constexpr int PX = XParts<TX>::n, PW = WParts<WMODE>::n;
-    constexpr int ROWB = KU * (int)sizeof(TX), RC = 1024 / ROWB, SLOT = 16 * MT * ROWB;   // bytes per row, rows per copy
+    constexpr int ROWB = KU * (int)sizeof(TX), RC = 1024 / ROWB;            // bytes per row, rows per copy
+    constexpr int XB = 16 * MT * ROWB, SLOT = XB + NT * (1024 + 256);               // X, codes, scales
     static_assert(XC * RC <= 16 * MT, "copies");
-    static_assert(2 * SLOT >= MT * NT * 1024, "the sums reuse X's space");
+    static_assert(D * SLOT >= MT * NT * 1024, "the sums reuse the ring's space");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     __shared__ Nf4Table tab;
     if constexpr (WMODE != W_INT4) {
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     // copy i: rows RC i .. of the unit; the 16-byte chunk c of row rho lies at
     // position c ^ (rho & 15), so 8 lanes that read one chunk of 8 rows meet 8
     // different positions
-    uint8_t *xl = lds + wave * 2 * SLOT;
+    uint8_t *xl = lds + wave * D * SLOT;
     const unsigned xlo = lds_offset(xl);
     unsigned xo[XC], xc[XC];
 #pragma unroll
@@ -54,34 +55,31 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
         xo[i] = (unsigned)min(row, mrows - 1) * ld;
         xc[i] = 16u * ((unsigned)(lane % (ROWB / 16)) ^ (row & 15));
     }
-    const uint8_t *c[NT];
-    const float *sc[NT];
+    // codes: lane l takes bytes 16 (l % 4) .. of row l / 4's 64; scales: lane l
+    // group l / 16 of row l % 16 of the unit
+    const int64_t row0 = rt.e * a.N + n0;
+    const uint8_t *cbase = a.codes + row0 * (K / 2);
+    const float *sbase = a.scales + row0 * ngroups;
+    const unsigned cc = 16u * (lane & 3), cend = (unsigned)(K / 2 - 16);
+    unsigned co[NT], so[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int64_t n = rt.e * a.N + min(n0 + 16 * j + r, a.N - 1);
-        c[j] = a.codes + n * (K / 2);
-        sc[j] = a.scales + n * ngroups;
+        co[j] = (unsigned)min(16 * j + (lane >> 2), a.N - n0 - 1) * (unsigned)(K / 2);
+        so[j] = (unsigned)min(16 * j + r, a.N - n0 - 1) * (unsigned)ngroups;
     }
-    // step h of a unit covers k = 32 h + 8 q .. + 7, within one group; the codes are
-    // loaded 16 bytes to a lane and transposed, the scales of up to 4 groups by the
-    // four groups of lanes
-    struct Unit {
-        unsigned c[NT][NH];
-        float s[NT];
-    };
-    constexpr int LOADS = XC + 2 * NT;                   // memory instructions of a unit
-    auto load = [&](int u, Unit &b) {
-        const int k0 = u * KU;
+    constexpr int LOADS = XC + 2 * NT;
+    auto issue = [&](int u, int slot) {
+        const unsigned at = xlo + slot * SLOT;
         // K % 128 left over (NG > 1): what lies past the row's end repeats it, to be zeroed
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
-            const unsigned at = (unsigned)u * ROWB + xc[i];
-            copy16_lds(xbase, xo[i] + (NG == 1 ? at : min(at, kbytes - 16)), xlo + (u & 1) * SLOT + 1024 * i);
+            const unsigned k = (unsigned)u * ROWB + xc[i];
+            copy16_lds(xbase, xo[i] + (NG == 1 ? k : min(k, kbytes - 16)), at + 1024 * i);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            __builtin_memcpy(&b.c[j][0], c[j] + min(k0 / 2 + 16 * q, K / 2 - 16), 16);
-            b.s[j] = sc[j][NG == 1 ? u : min((k0 >> lg) + q, ngroups - 1)];
+            copy16_lds(cbase, co[j] + min((unsigned)u * (KU / 2) + cc, cend), at + XB + 1024 * j);
+            copy4_lds(sbase, 4u * (so[j] + (NG == 1 ? u : min(((u * KU) >> lg) + q, ngroups - 1))), at + XB + NT * 1024 + 256 * j);
         }
     };
     f32x4 acc[MT][NT];
@@ -89,10 +87,18 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{};
-    auto multiply = [&](int u, Unit &b) {
-        const uint8_t *xs = xl + (u & 1) * SLOT + r * ROWB;
+    // step h of a unit covers k = 32 h + 8 q .. + 7, within one group: the lane's 16
+    // bytes of codes, transposed
+    auto multiply = [&](int u, int slot) {
+        const uint8_t *us = xl + slot * SLOT, *xs = us + r * ROWB;
+        unsigned c[NT][NH];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) transpose4(b.c[j]);
+        for (int j = 0; j < NT; ++j) {
+            const u32x4 v = *(const u32x4 *)(us + XB + 1024 * j + 64 * r + 16 * q);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) c[j][h] = v[h];
+            transpose4(c[j]);
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f32x4 part[MT][NT] = {};
@@ -100,7 +106,7 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
             for (int h = g * (NH / NG); h < (g + 1) * (NH / NG); ++h) {
                 bf16x8 wp[NT][PW];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) code_parts<WMODE>(b.c[j][h], tab, wp[j]);
+                for (int j = 0; j < NT; ++j) code_parts<WMODE>(c[j][h], tab, wp[j]);
                 const bool in = NG == 1 || u * KU + 32 * h < K;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -117,7 +123,7 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const float s = (NG == 1 ? b.s[j] : __shfl(b.s[j], r + 16 * g)) * (1.0f / CodeScale<WMODE>::v);
+                const float s = *(const float *)(us + XB + NT * 1024 + 256 * j + 4 * (r + 16 * g)) * (1.0f / CodeScale<WMODE>::v);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -127,19 +133,7 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     };
     const int units = (K + KU - 1) / KU, per = (units + W - 1) / W;
     const int u0 = wave * per, u1 = min(u0 + per, units);
-    if (u0 < u1) {
-        Unit cur, nxt;
-        load(u0, cur);
-        for (int u = u0; u + 1 < u1; ++u) {
-            asm volatile("" ::: "memory");               // the other slot's reads are done
-            load(u + 1, nxt);
-            wait_copies<LOADS>();                        // unit u's are in
-            multiply(u, cur);
-            cur = nxt;
-        }
-        wait_copies<0>();
-        multiply(u1 - 1, cur);
-    }
+    ring<D, LOADS>(u0, u1, issue, multiply);
     __syncthreads();                                     // every wave is past its X
     float *red = (float *)lds;                           // [W][MT * NT * 256]
 #pragma unroll
@@ -159,10 +153,11 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     }
 }
 
-template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC> hipError_t launch(const I4Args &a, hipStream_t s)
+template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC, int D> hipError_t launch(const I4Args &a, hipStream_t s)
 {
-    constexpr size_t lds = (size_t)W * 2 * 16 * MT * KU * sizeof(TX);
-    const auto kernel = int4_skinny_kernel<TX, WMODE, NG, MT, NT, W, XC>;
+    constexpr size_t lds = (size_t)W * D * (16 * MT * KU * sizeof(TX) + NT * (1024 + 256));
+    static_assert(lds + sizeof(Nf4Table) <= 160 * 1024, "LDS");
+    const auto kernel = int4_skinny_kernel<TX, WMODE, NG, MT, NT, W, XC, D>;
     static const bool lds_ok =
         hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
     if (!lds_ok) return hipErrorInvalidConfiguration;
@@ -176,9 +171,10 @@ template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC> hipErro
 template <typename TX, int WMODE, int NG> hipError_t by_rows(const I4Args &a, int shape, hipStream_t s)
 {
     constexpr int C16 = 16 * KU * (int)sizeof(TX) / 1024;        // copies for 16 rows
-    if (shape == 2) return launch<TX, WMODE, NG, 2, 2, 4, 2 * C16>(a, s);
-    if (a.M <= 4) return shape ? launch<TX, WMODE, NG, 1, 2, 8, C16 / 4>(a, s) : launch<TX, WMODE, NG, 1, 1, 8, C16 / 4>(a, s);
-    return shape ? launch<TX, WMODE, NG, 1, 2, 8, C16>(a, s) : launch<TX, WMODE, NG, 1, 1, 8, C16>(a, s);
+    constexpr int D = 2;        // deeper rings leave fewer workgroups to a CU: 13.4 / 14.0 / 17.7 us for 2, 3, 4 at 16 x 10240 x 5120
+    if (shape == 2) return launch<TX, WMODE, NG, 2, 2, 4, 2 * C16, D>(a, s);
+    if (a.M <= 4) return shape ? launch<TX, WMODE, NG, 1, 2, 4, C16 / 4, D>(a, s) : launch<TX, WMODE, NG, 1, 1, 4, C16 / 4, D>(a, s);
+    return shape ? launch<TX, WMODE, NG, 1, 2, 4, C16, D>(a, s) : launch<TX, WMODE, NG, 1, 1, 4, C16, D>(a, s);
 }
 
 template <typename TX, int WMODE> hipError_t by_group(const I4Args &a, int shape, hipStream_t s)

@@ -137,6 +137,44 @@ template <int N = 0> __device__ inline void wait_copies()
     static_assert(N >= 0 && N < 64, "vmcnt");
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+// Waits for this wave's LDS reads (and writes): before a copy may overwrite them.
+__device__ inline void wait_lds()
+{
+    __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), the other counters at their maxima
+    asm volatile("" ::: "memory");
+}
+
+// Runs the units u0 .. u1 - 1 of a wave through a ring of D slots of its own part
+// of LDS: issue(u, slot) starts the LOADS copies of a unit, use(u, slot) consumes
+// it.  D - 1 units are under way while one is used.  Only copies (which the
+// compiler does not know of) load from memory in here, so that the waits are
+// these alone.
+template <int D, int LOADS, typename Issue, typename Use> __device__ inline void ring(int u0, int u1, Issue issue, Use use)
+{
+    static_assert(D >= 2 && D <= 4 && (D - 1) * LOADS < 64, "vmcnt");
+    int in = 0;                                      // slot of the next unit to issue
+    int u = u0;
+    for (; u < u0 + D - 1 && u < u1; ++u) issue(u, in++);
+    int out = 0;
+    for (int v = u0; v < u1; ++v) {
+        if (u < u1) {
+            wait_lds();
+            issue(u, in);
+            ++u;
+            in = in + 1 == D ? 0 : in + 1;
+            wait_copies<(D - 1) * LOADS>();
+        } else {
+            // the last units: fewer are under way
+            const int left = u1 - 1 - v;
+            if (D > 3 && left >= 2) wait_copies<2 * LOADS>();
+            else if (D > 2 && left >= 1) wait_copies<LOADS>();
+            else wait_copies<0>();
+        }
+        use(v, out);
+        out = out + 1 == D ? 0 : out + 1;
+    }
+}
+
 __device__ inline void publish()
 {
     wait_copies();
