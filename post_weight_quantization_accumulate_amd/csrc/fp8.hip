@@ -1,5 +1,7 @@
 // fp8.hip -- 8-bit floating point (e4m3) packs with one scale per block of 128
 // columns, and products of two of them.
+#include <algorithm>
+
 #include "gq.h"
 #include "gq_internal.h"
 #include "gemv.h"
@@ -471,8 +473,29 @@ template <typename TY> hipError_t launch_fp8(F8Args a, hipStream_t s)
     v.y_bf16 = sizeof(TY) == 2;
     const int64_t rows = a.offsets ? (a.M + a.E - 1) / a.E : a.M;
     if (rows <= kGemvMaxRows && gemv_ok(v, GEMV_FP8, (int)rows)) return launch_gemv(v, GEMV_FP8, (int)rows, s);
-    if (dma && rows <= 64) return launch_skinny<TY, 1, 1, 4, 2>(a, s);
-    return dma ? launch_tile<TY, 2, 4, 8, 4, true>(a, s) : launch_tile<TY, 2, 4, 8, 4, false>(a, s);
+    // Time of the whole grid, in us at K = 5120 (it grows with K alike): rounds of
+    // tiles over the CUs.  16 x 16, 16 x 32 and 32 x 32 with K split over the waves:
+    // 4, 6 and 8 us a round; 64 x 128, three workgroups to a CU: 42 us up to two of
+    // them, then 54 us for every three; 256 x 256: 114 us a round (measured at
+    // M = 3 .. 8192, N = 1024 .. 10240).
+    const bool ex = a.offsets != nullptr;
+    auto tiles = [&](int64_t tm, int64_t tn) { return (a.N + tn - 1) / tn * row_tiles(ex, a.E, a.M, tm); };
+    auto rounds = [](int64_t t) { return (double)((t + 255) / 256); };
+    const double small[3] = {4 * rounds(tiles(16, 16)), 6 * rounds(tiles(16, 32)), 8 * rounds(tiles(32, 32))};
+    const int64_t tmid = tiles(64, 128);
+    const double mid = tmid <= 512 ? 42 : 54 * std::max(1.0, (double)tmid / 768);
+    const int best = small[2] < small[0] ? (small[2] < small[1] ? 2 : 1) : (small[1] < small[0] ? 1 : 0);
+    if (dma && small[best] < mid) {
+        if (best == 0) return launch_skinny<TY, 1, 1, 4, 2>(a, s);
+        if (best == 1) return launch_skinny<TY, 1, 2, 8, 2>(a, s);
+        return launch_skinny<TY, 2, 2, 4, 2>(a, s);
+    }
+    // the large tile's sums leave no registers for codes turned into bf16
+    if constexpr (sizeof(TY) == 2) {
+        if (114 * rounds(tiles(256, 256)) < mid)
+            return dma ? launch_tile<TY, 2, 4, 8, 4, true>(a, s) : launch_tile<TY, 2, 4, 8, 4, false>(a, s);
+    }
+    return dma ? launch_tile<TY, 1, 4, 4, 2, true>(a, s) : launch_tile<TY, 1, 4, 4, 2, false>(a, s);
 }
 
 }  // namespace
