@@ -186,15 +186,15 @@ template <typename TX, int WMODE> hipError_t by_group(const I4Args &a, int shape
 
 }  // namespace
 
-// Time of the whole grid in units of a 16 x 16 tile's fixed part: one tile per CU
-// at a time, tiles of 16 x 16, 16 x 32 and 32 x 32 costing 2, 3 and 4.
-int64_t int4_skinny_cost(const I4Args &a, int *shape)
+// One tile per CU at a time; a round of tiles of 16 x 16, 16 x 32 or 32 x 32 takes
+// 4, 6 or 8 us.
+double int4_skinny_cost(const I4Args &a, int *shape)
 {
-    int64_t best = 0;
+    double best = 0;
     for (int i = 0; i < 3; ++i) {
         const int64_t tm = i == 2 ? 32 : 16, tn = i ? 32 : 16;
         const int64_t tiles = (a.N + tn - 1) / tn * row_tiles(a.offsets != nullptr, a.E, a.M, tm);
-        const int64_t c = (tiles + 255) / 256 * (2 + i);
+        const double c = (double)((tiles + 255) / 256 * (4 + 2 * i));
         if (i == 0 || c < best) { best = c; *shape = i; }
     }
     return best;

@@ -167,24 +167,55 @@ template <typename TX, int WMODE, int NG, int PM, int PN> hipError_t launch(cons
     return hipGetLastError();
 }
 
-// The weights' bf16 parts of a stage stay in registers beside the sums: 64
-// columns per wave fit with one part and up to two scales per stage, else 32.
-template <typename TX, int WMODE> hipError_t by_group(const I4Args &a, hipStream_t s)
+// Tile shapes by number: 128 x 256, 128 x 128, 96 x 128, 64 x 128.  The weights'
+// bf16 parts of a stage stay in registers beside the sums: 256 columns fit with
+// one part and up to two scales per stage.
+template <typename TX, int WMODE, int NG> hipError_t by_shape(const I4Args &a, int shape, hipStream_t s)
 {
-    constexpr int KS = kRow / (int)sizeof(TX), PN = WMODE == W_INT4 ? 4 : 2;
-    if (a.G >= KS) return launch<TX, WMODE, 1, 8, PN>(a, s);
-    if (2 * a.G == KS) return launch<TX, WMODE, 2, 8, PN>(a, s);
-    if constexpr (KS == 128) return launch<TX, WMODE, 4, 8, 2>(a, s);
+    if constexpr (WMODE == W_INT4 && NG <= 2) {
+        if (shape == 0) return launch<TX, WMODE, NG, 8, 4>(a, s);
+    }
+    if (shape <= 1) return launch<TX, WMODE, NG, 8, 2>(a, s);
+    if (shape == 2) return launch<TX, WMODE, NG, 6, 2>(a, s);
+    return launch<TX, WMODE, NG, 4, 2>(a, s);
+}
+
+template <typename TX, int WMODE> hipError_t by_group(const I4Args &a, int shape, hipStream_t s)
+{
+    constexpr int KS = kRow / (int)sizeof(TX);
+    if (a.G >= KS) return by_shape<TX, WMODE, 1>(a, shape, s);
+    if (2 * a.G == KS) return by_shape<TX, WMODE, 2>(a, shape, s);
+    if constexpr (KS == 128) return by_shape<TX, WMODE, 4>(a, shape, s);
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s)
+// The larger tile does less work per product, the smaller leaves fewer CUs idle.
+// `slots` workgroups of a shape run at a time; a round of up to 256 takes `few`
+// us, a full one `full` (bf16 rows, K = 5120, measured at M = 128 .. 8192).
+double int4_tile_cost(const I4Args &a, bool x_bf16, bool nf4, int *shape)
 {
-    if (!x_bf16) return nf4 ? by_group<float, W_NF4_3>(a, s) : by_group<float, W_INT4>(a, s);
-    if (!nf4) return by_group<__bf16, W_INT4>(a, s);
-    return a.y_bf16 ? by_group<__bf16, W_NF4_2>(a, s) : by_group<__bf16, W_NF4_3>(a, s);
+    static const struct { int tm, tn, slots; double few, full; } kShapes[4] = {
+        {128, 256, 512, 133, 160}, {128, 128, 512, 82, 86}, {96, 128, 768, 63, 98}, {64, 128, 1024, 52, 104}};
+    const bool wide = !nf4 && a.G >= (x_bf16 ? 64 : 32);
+    double best = 0;
+    for (int i = wide ? 0 : 1; i < 4; ++i) {
+        const auto &k = kShapes[i];
+        const int64_t t = (a.N + k.tn - 1) / k.tn * row_tiles(a.offsets != nullptr, a.E, a.M, k.tm);
+        const int64_t rem = t % k.slots;
+        double c = (double)(t / k.slots) * k.full;
+        if (rem) c += rem <= 256 ? k.few : k.few + (k.full - k.few) * (double)(rem - 256) / (double)(k.slots - 256);
+        if (best == 0 || c < best) { best = c; *shape = i; }
+    }
+    return best;
+}
+
+hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, int shape, hipStream_t s)
+{
+    if (!x_bf16) return nf4 ? by_group<float, W_NF4_3>(a, shape, s) : by_group<float, W_INT4>(a, shape, s);
+    if (!nf4) return by_group<__bf16, W_INT4>(a, shape, s);
+    return a.y_bf16 ? by_group<__bf16, W_NF4_2>(a, shape, s) : by_group<__bf16, W_NF4_3>(a, shape, s);
 }
 
 }  // namespace gq

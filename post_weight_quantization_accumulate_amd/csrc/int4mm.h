@@ -123,10 +123,13 @@ __device__ inline void store_row(const I4Args &a, int64_t row, int n, float v)
     else ((float *)a.Y)[row * a.ldy + n] = v;
 }
 
-// Groups of 32 and more, any M, K, strides and alignment (int4_tile.hip).
-hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s);
-// The same for few rows (int4_skinny.hip).
-int64_t int4_skinny_cost(const I4Args &a, int *shape);
+// Groups of 32 and more, any M, K, strides and alignment (int4_tile.hip), and the
+// same for few rows, aligned to 16 bytes (int4_skinny.hip).  The costs are
+// estimates of the time in us of bf16 rows at K = 5120, for choosing between the
+// tile shapes and the two; they grow alike with K and the types.
+double int4_tile_cost(const I4Args &a, bool x_bf16, bool nf4, int *shape);
+hipError_t launch_int4_tile(const I4Args &a, bool x_bf16, bool nf4, int shape, hipStream_t s);
+double int4_skinny_cost(const I4Args &a, int *shape);
 hipError_t launch_int4_skinny(const I4Args &a, bool x_bf16, bool nf4, int shape, hipStream_t s);
 
 }  // namespace gq

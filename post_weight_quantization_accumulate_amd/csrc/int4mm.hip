@@ -116,15 +116,11 @@ hipError_t launch_int4(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s)
     v.y_bf16 = a.y_bf16; v.x_bf16 = x_bf16;
     const int kind = nf4 ? GEMV_NF4 : GEMV_INT4;
     if (rows <= kGemvMaxRows && gemv_ok(v, kind, (int)rows)) return launch_gemv(v, kind, (int)rows, s);
-    // Small tiles with K split over the waves, or large ones: in the units of
-    // int4_skinny_cost, a round of 128 x 256 tiles takes 66 with one workgroup to
-    // a CU and 78 with two (K = 5120: 131 and 157 us, against 2 us).
-    int shape = 0;
-    const int64_t large = (a.N + 255) / 256 * row_tiles(a.offsets != nullptr, a.E, a.M, 128);
-    const int64_t large_cost = large <= 256 ? 66 : (large + 511) / 512 * 78;
+    int small = 0, large = 0;
+    const double cost = int4_tile_cost(a, x_bf16, nf4, &large);
     const bool aligned = ((uintptr_t)a.X & 15) == 0 && (a.ldx * (x_bf16 ? 2 : 4)) % 16 == 0;
-    if (aligned && int4_skinny_cost(a, &shape) < large_cost) return launch_int4_skinny(a, x_bf16, nf4, shape, s);
-    return launch_int4_tile(a, x_bf16, nf4, s);
+    if (aligned && int4_skinny_cost(a, &small) < cost) return launch_int4_skinny(a, x_bf16, nf4, small, s);
+    return launch_int4_tile(a, x_bf16, nf4, large, s);
 }
 
 }  // namespace
