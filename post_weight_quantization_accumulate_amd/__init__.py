@@ -497,6 +497,15 @@ def _launch(name, first, others, *args):
         _check(status, name)
 
 
+def _experts(offsets):
+    """E of offsets (E + 1 int32)."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        raise ValueError("offsets must be a 1-D tensor of E + 1 entries")
+    E = offsets.shape[0] - 1
+    _shape(offsets, "offsets", torch.int32, (E + 1,))
+    return E
+
+
 def _group_ok(group, K):
     if group < 1 or K % group:
         raise ValueError(f"group {group} does not divide K = {K}")
@@ -522,9 +531,8 @@ def int4_matmul_experts(Y, X, codes, scales, offsets, group: int, flags: int = 0
     yd, ldy = _rows(Y, "Y")
     M, N = Y.shape
     xd, ldx = _rows(X, "X", M)
-    K, E = X.shape[1], offsets.numel() - 1
+    K, E = X.shape[1], _experts(offsets)
     _group_ok(group, K)
-    _shape(offsets, "offsets", torch.int32, (E + 1,))
     _shape(codes, "codes", torch.uint8, (E, N, K // 2))
     _shape(scales, "scales", torch.float32, (E, N, K // group))
     _launch("int4_matmul_experts", Y, (X, codes, scales, offsets), Y.data_ptr(), yd, ldy, X.data_ptr(), xd, ldx,
@@ -564,9 +572,8 @@ def fp8_matmul_experts(Y, Xq, xs, Wq, ws, offsets) -> None:
     E x ceil(N/128) x ceil(K/128), offsets E + 1 int32 (experts_sort's)."""
     yd, ldy = _rows(Y, "Y")
     M, N = Y.shape
-    K, E = Xq.shape[-1], offsets.numel() - 1
+    K, E = Xq.shape[-1], _experts(offsets)
     kb = -(-K // 128)
-    _shape(offsets, "offsets", torch.int32, (E + 1,))
     _shape(Xq, "Xq", torch.float8_e4m3fn, (M, K))
     _shape(xs, "xs", torch.float32, (M, kb))
     _shape(Wq, "Wq", torch.float8_e4m3fn, (E, N, K))
@@ -585,11 +592,10 @@ def experts_sort(offsets, order, pos, ids, ws=None) -> None:
     offsets.numel() - 1 experts: offsets (E + 1), order (T k, each row's slot) and
     pos (like ids, each slot's row or -1), all int32.  ws: experts_sort_workspace_size
     bytes, None where that is 0."""
-    n, E = ids.numel(), offsets.numel() - 1
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise ValueError("ids must be int32 or int64")
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be an int32 or int64 tensor")
+    n, E = ids.numel(), _experts(offsets)
     _shape(ids, "ids", ids.dtype, tuple(ids.shape))
-    _shape(offsets, "offsets", torch.int32, (E + 1,))
     _shape(order, "order", torch.int32, (n,))
     _shape(pos, "pos", torch.int32, tuple(ids.shape))
     if ws is not None:

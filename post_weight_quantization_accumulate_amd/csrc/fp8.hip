@@ -297,10 +297,9 @@ template <typename TY, int MT, int NT, int W, int D> hipError_t launch_skinny(co
 {
     constexpr size_t lds = (size_t)W * D * (2048 * (MT + NT) + 256 * MT);
     static_assert(lds <= 160 * 1024, "LDS");
-    const auto kernel = fp8_skinny_kernel<TY, MT, NT, W, D>;
-    static const bool lds_ok =
-        hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
-    if (!lds_ok) return hipErrorInvalidConfiguration;
+    constexpr auto kernel = fp8_skinny_kernel<TY, MT, NT, W, D>;
+    const hipError_t e = allow_lds<kernel>(lds);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, tile_grid((a.N + 16 * NT - 1) / (16 * NT), row_tiles(a.offsets != nullptr, a.E, a.M, 16 * MT)),
                        dim3(64 * W), lds, s, a);
     return hipGetLastError();
@@ -451,6 +450,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(F8Args a, int64_
         for (int j = 0; j < PN; ++j)
 #pragma unroll
             for (int t = 0; t < 4; ++t) acc[PM - 1][j][t] = fmaf(s[1], part[1][j][t], acc[PM - 1][j][t]);
+        wait_copies();                                   // the last stage's: none outlives the workgroup
     } else {
         for (int b = 0; b < kb; ++b) {
             const int slot = b & 1;
@@ -507,10 +507,11 @@ hipError_t launch_tile(const F8Args &a, hipStream_t s)
 {
     constexpr int TM = 16 * WM * PM, TN = 16 * WN * PN;
     constexpr size_t lds = 2 * ((size_t)(TM + TN) * kStage + TM * sizeof(float));
-    const auto kernel = fp8_tile_kernel<TY, WM, WN, PM, PN, DMA, sizeof(TY) == 2>;
-    static const bool lds_ok = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
-    if (!lds_ok) return hipErrorInvalidConfiguration;
+    constexpr auto kernel = fp8_tile_kernel<TY, WM, WN, PM, PN, DMA, sizeof(TY) == 2>;
+    const hipError_t e = allow_lds<kernel>(lds);
+    if (e != hipSuccess) return e;
     const int64_t nt = (a.N + TN - 1) / TN, mt = row_tiles(a.offsets != nullptr, a.E, a.M, TM);
+    if (!grid_fits(nt * mt, 64 * WM * WN)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(nt * mt)), dim3(64 * WM * WN), lds, s, a, nt, mt);
     return hipGetLastError();
 }

@@ -157,10 +157,9 @@ template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC, int D> 
 {
     constexpr size_t lds = (size_t)W * D * (16 * MT * KU * sizeof(TX) + NT * (1024 + 256));
     static_assert(lds + sizeof(Nf4Table) <= 160 * 1024, "LDS");
-    const auto kernel = int4_skinny_kernel<TX, WMODE, NG, MT, NT, W, XC, D>;
-    static const bool lds_ok =
-        hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
-    if (!lds_ok) return hipErrorInvalidConfiguration;
+    constexpr auto kernel = int4_skinny_kernel<TX, WMODE, NG, MT, NT, W, XC, D>;
+    const hipError_t e = allow_lds<kernel>(lds);
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, tile_grid((a.N + 16 * NT - 1) / (16 * NT), row_tiles(a.offsets != nullptr, a.E, a.M, 16 * MT)),
                        dim3(64 * W), lds, s, a);
     return hipGetLastError();

@@ -157,12 +157,12 @@ template <typename TX, int WMODE, int NG, int PM, int PN> hipError_t launch(cons
 {
     constexpr int TM = 16 * PM, TN = 64 * PN;
     constexpr size_t lds = 2 * (size_t)TM * kRow;
-    const auto kernel = int4_tile_kernel<TX, WMODE, NG, PM, PN>;
-    static const bool lds_ok =
-        hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess;
-    if (!lds_ok) return hipErrorInvalidConfiguration;
+    constexpr auto kernel = int4_tile_kernel<TX, WMODE, NG, PM, PN>;
+    const hipError_t e = allow_lds<kernel>(lds);
+    if (e != hipSuccess) return e;
     const bool dma = ((uintptr_t)a.X & 15) == 0 && (a.ldx * sizeof(TX)) % 16 == 0;
     const int64_t nt = (a.N + TN - 1) / TN, mt = row_tiles(a.offsets != nullptr, a.E, a.M, TM);
+    if (!grid_fits(nt * mt, 256)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(nt * mt)), dim3(256), lds, s, a, nt, mt, dma);
     return hipGetLastError();
 }

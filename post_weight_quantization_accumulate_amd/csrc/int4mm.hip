@@ -118,7 +118,7 @@ hipError_t launch_int4(const I4Args &a, bool x_bf16, bool nf4, hipStream_t s)
     if (rows <= kGemvMaxRows && gemv_ok(v, kind, (int)rows)) return launch_gemv(v, kind, (int)rows, s);
     int small = 0, large = 0;
     const double cost = int4_tile_cost(a, x_bf16, nf4, &large);
-    const bool aligned = ((uintptr_t)a.X & 15) == 0 && (a.ldx * (x_bf16 ? 2 : 4)) % 16 == 0;
+    const bool aligned = ((uintptr_t)a.X & 15) == 0 && (a.ldx * (x_bf16 ? 2 : 4)) % 16 == 0 && ((uintptr_t)a.codes & 15) == 0;
     if (aligned && int4_skinny_cost(a, &small) < cost) return launch_int4_skinny(a, x_bf16, nf4, small, s);
     return launch_int4_tile(a, x_bf16, nf4, large, s);
 }

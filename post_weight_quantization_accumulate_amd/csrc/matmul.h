@@ -4,6 +4,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <atomic>
 #include <stdint.h>
 
 #include "gq_internal.h"
@@ -66,6 +67,24 @@ __device__ inline bool row_tile(const int *offsets, int E, int64_t M, int TM, in
     }
     return false;
 }
+
+// Lets Kernel use `bytes` of dynamic LDS on the current device (asked for once per
+// device).
+template <auto Kernel> hipError_t allow_lds(size_t bytes)
+{
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    const hipError_t f = hipFuncSetAttribute((const void *)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (f == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return f;
+}
+
+// A launch holds fewer than 2^32 threads in a dimension.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
 
 // An upper bound of the number of row tiles: with experts every tile holds a
 // row and every expert adds at most one partly filled tile.
@@ -186,22 +205,6 @@ __device__ inline unsigned lds_offset(const void *p)
 {
     return (unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
-
-// Loads through a buffer descriptor: `bytes` from p, anything past them reads as
-// zero without touching memory, so a load can be left out by its offset, with no
-// branch around it (a branch makes the compiler wait for every load in flight).
-// Dword aligned.
-typedef __amdgpu_buffer_rsrc_t Buffer;
-constexpr unsigned kNoLoad = 0xFFFFFFF0u;
-__device__ inline Buffer make_buffer(const void *p, unsigned bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, bytes, 0x00027000);   // raw, 32-bit data
-}
-__device__ inline u32x4 buffer_load16(Buffer b, unsigned off)
-{
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
-}
-__device__ inline unsigned buffer_load4(Buffer b, unsigned off) { return __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0); }
 
 // 16 bytes from p, of which only the first n are the caller's (the rest zero);
 // p may be unaligned.

@@ -77,39 +77,50 @@ def _int4(gq, M, N, K, G, nf4, xd, yd, seed, padx=0, pady=0):
                                      (16, 48, 640, 128), (64, 256, 1024, 128), (65, 300, 192, 64), (130, 257, 256, 16),
                                      (300, 130, 512, 128), (257, 515, 2176, 128), (5, 16, 2, 1), (2, 1000, 5120, 128),
                                      (33, 272, 1152, 128), (600, 520, 384, 128), (100, 70, 160, 32), (129, 65, 32, 32),
-                                     (200, 129, 320, 64), (20, 40, 224, 32), (50, 40, 320, 64)])
+                                     (200, 129, 320, 64), (20, 40, 224, 32), (50, 40, 320, 64), (1, 20, 17408, 128),
+                                     (1, 24, 33280, 128), (2, 16, 20608, 64), (1, 40, 96, 32), (20, 70, 64, 16)])
 def test_int4_matmul(gq, M, N, K, G, nf4, xd, yd):
     _int4(gq, M, N, K, G, nf4, xd, yd, M * 31 + N + K)
 
 
-@pytest.mark.parametrize("M,N,K,G,padx,pady", [(5, 64, 256, 128, 3, 5), (70, 128, 256, 64, 8, 8), (300, 256, 256, 128, 1, 0),
+@pytest.mark.parametrize("xd,nf4,G", [("bf16", False, 128), ("bf16", False, 64), ("bf16", False, 32), ("bf16", True, 128),
+                                      ("fp32", False, 128), ("fp32", True, 32)])
+@pytest.mark.parametrize("M,N", [(4000, 4090), (2040, 4090), (1000, 5000), (250, 10200)])
+def test_int4_matmul_every_tile(gq, M, N, xd, nf4, G):
+    """Sizes at which each shape of the many-row kernel is chosen, with ragged edges."""
+    _int4(gq, M, N, 256, G, nf4, xd, xd, M + G)
+
+
+@pytest.mark.parametrize("M,N,K,G,padx,pady", [(5, 64, 256, 128, 3, 5), (70, 128, 256, 64, 8, 8), (2, 64, 256, 128, 3, 5), (300, 256, 256, 128, 1, 0),
                                                (300, 256, 256, 128, 8, 1)])
 @pytest.mark.parametrize("xd", ["bf16", "fp32"])
 def test_int4_matmul_strides(gq, M, N, K, G, padx, pady, xd):
     _int4(gq, M, N, K, G, False, xd, xd, 5, padx, pady)
 
 
-def test_int4_matmul_unaligned_bases(gq):
+@pytest.mark.parametrize("M", [1, 20, 100])
+@pytest.mark.parametrize("xoff", [0, 1])
+def test_int4_matmul_unaligned_bases(gq, M, xoff):
     """Pointers that are only element aligned: X two bytes, the codes one byte off."""
     rng = np.random.default_rng(1)
-    M, N, K, G = 20, 48, 256, 128
+    N, K, G = 48, 256, 128
     x = _x(rng, M, K, torch.bfloat16)
     codes, scales = _pack4(rng, N, K, G)
-    xb = torch.zeros(M * K + 1, dtype=torch.bfloat16, device=DEV)
-    xb[1:] = x.to(DEV).reshape(-1)
+    xb = torch.zeros(M * K + xoff, dtype=torch.bfloat16, device=DEV)
+    xb[xoff:] = x.to(DEV).reshape(-1)
     cb = torch.zeros(N * K // 2 + 1, dtype=torch.uint8, device=DEV)
     cb[1:] = torch.from_numpy(codes).to(DEV).reshape(-1)
     sb = torch.zeros(N * K // G + 1, device=DEV)
     sb[1:] = torch.from_numpy(scales).to(DEV).reshape(-1)
     yb = torch.zeros(M * N + 1, device=DEV)
-    gq.int4_matmul(yb[1:].view(M, N), xb[1:].view(M, K), cb[1:].view(N, K // 2), sb[1:].view(N, K // G), G)
+    gq.int4_matmul(yb[1:].view(M, N), xb[xoff:].view(M, K), cb[1:].view(N, K // 2), sb[1:].view(N, K // G), G)
     w = _deq4(gq, codes, scales, G, False)
     x64 = x.double().numpy()
     _check(yb[1:].view(M, N), x64 @ w.T, np.abs(x64) @ np.abs(w).T, K)
 
 
 @pytest.mark.parametrize("xd", ["bf16", "fp32"])
-@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("M", [2, 4, 20, 300])
 def test_int4_matmul_special_values(gq, xd, M):
     """NaN and infinity spread along their own row only; huge and tiny values survive the split into parts."""
     rng = np.random.default_rng(2)
@@ -134,7 +145,8 @@ def test_int4_matmul_special_values(gq, xd, M):
 
 @pytest.mark.parametrize("counts,M", [([0, 5, 0, 17, 1, 40], 63), ([3], 3), ([0, 0, 0], 4), ([16] * 8, 128),
                                       ([1] * 70, 70), ([300, 0, 2, 257], 560), ([0, 700], 700), ([513, 31, 64], 608)])
-@pytest.mark.parametrize("nf4,xd,G", [(False, "bf16", 128), (True, "fp32", 64), (False, "fp32", 32), (True, "bf16", 128)])
+@pytest.mark.parametrize("nf4,xd,G", [(False, "bf16", 128), (True, "fp32", 64), (False, "fp32", 32), (True, "bf16", 128),
+                                      (False, "bf16", 16)])
 def test_int4_matmul_experts(gq, counts, M, nf4, xd, G):
     """Ragged and empty experts; rows behind the last are left as they were."""
     rng = np.random.default_rng(M)
@@ -253,7 +265,9 @@ def _deq8(codes, scales, br):
 @pytest.mark.parametrize("yd", ["bf16", "fp32"])
 @pytest.mark.parametrize("M,N,K", [(1, 16, 128), (1, 1, 1), (3, 200, 100), (16, 128, 256), (33, 130, 1000),
                                    (64, 300, 1024), (65, 257, 129), (130, 256, 640), (300, 384, 512), (257, 515, 2176),
-                                   (513, 260, 136), (2, 1024, 5120), (600, 512, 384), (40, 1000, 4100)])
+                                   (513, 260, 136), (2, 1024, 5120), (600, 512, 384), (40, 1000, 4100),
+                                   (33, 130, 1008), (5, 64, 144), (17, 40, 16), (1, 30, 17408), (1, 20, 33280), (2, 24, 20608),
+                                   (1, 40, 96), (3, 50, 640), (4200, 260, 256), (700, 2050, 128)])
 def test_fp8_matmul(gq, M, N, K, yd):
     rng = np.random.default_rng(M + N + K)
     xq, xs = _pack8(gq, _x(rng, M, K, torch.float32), 1)
@@ -263,6 +277,29 @@ def test_fp8_matmul(gq, M, N, K, yd):
     x, w = _deq8(xq, xs, 1), _deq8(wq, ws, 128)
     _check(y[:, :N], x @ w.T, np.abs(x) @ np.abs(w).T, K, cut=2.0 ** -10 if yd == "bf16" else 0.0)
     assert (y[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("yd", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(4090, 2810, 384), (4090, 2810, 128), (4090, 2810, 200)])
+def test_fp8_matmul_large_tile(gq, M, N, K, yd):
+    """Enough rows and columns for 256 x 256 tiles (whole blocks of k, bf16), with ragged edges."""
+    test_fp8_matmul(gq, M, N, K, yd)
+
+
+def test_fp8_matmul_experts_large_tile(gq):
+    rng = np.random.default_rng(8)
+    counts, N, K = [2500, 0, 1700], 2816, 256
+    M, off = 4210, np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    xq, xs = _pack8(gq, _x(rng, M, K, torch.float32), 1)
+    packs = [_pack8(gq, _x(rng, N, K, torch.float32) * 0.02, 128) for _ in counts]
+    y = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    gq.fp8_matmul_experts(y, xq, xs, torch.stack([p[0].view(torch.uint8) for p in packs]).view(torch.float8_e4m3fn),
+                          torch.stack([p[1] for p in packs]), torch.from_numpy(off).to(DEV))
+    x = _deq8(xq, xs, 1)
+    for e in (0, 2):
+        a, z, w = off[e], off[e + 1], _deq8(*packs[e], 128)
+        _check(y[a:z], x[a:z] @ w.T, np.abs(x[a:z]) @ np.abs(w).T, K, e, 2.0 ** -10)
+    assert (y[off[-1]:] == 7.0).all()
 
 
 @pytest.mark.parametrize("yd", ["bf16", "fp32"])
@@ -287,7 +324,7 @@ def test_fp8_matmul_experts(gq, counts, M, N, K, yd):
     assert (y[off[-1]:] == 7.0).all()
 
 
-@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("M", [2, 20, 300])
 def test_fp8_matmul_nan_stays_in_its_row(gq, M):
     rng = np.random.default_rng(4)
     x = _x(rng, M, 256, torch.float32)
