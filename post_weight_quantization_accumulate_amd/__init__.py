@@ -462,8 +462,10 @@ def _rows(t, name, rows=None, cols=None):
     r, c = t.shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} is {r} x {c}, needs {r if rows is None else rows} x {c if cols is None else cols}")
-    ld = t.stride(0) if r > 1 else c
-    if (c > 1 and t.stride(1) != 1) or ld < c:
+    ld, unit = t.stride()
+    if r <= 1:
+        ld = c
+    if (c > 1 and unit != 1) or ld < c:
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
     return dt, ld
 
@@ -474,8 +476,8 @@ def _shape(t, name, dtype, shape):
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -486,9 +488,9 @@ def _launch(name, first, others, *args):
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: every tensor must be on cuda:{dev}")
-    # the raw handle: a Stream object costs 2 us, a third of a small call
+    # raw handles: a Stream object costs 2 us, a third of a small call
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = getattr(lib(), name)(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -595,9 +597,9 @@ def experts_sort(offsets, order, pos, ids, ws=None) -> None:
     if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be an int32 or int64 tensor")
     n, E = ids.numel(), _experts(offsets)
-    _shape(ids, "ids", ids.dtype, tuple(ids.shape))
+    _shape(ids, "ids", ids.dtype, ids.shape)
     _shape(order, "order", torch.int32, (n,))
-    _shape(pos, "pos", torch.int32, tuple(ids.shape))
+    _shape(pos, "pos", torch.int32, ids.shape)
     if ws is not None:
         _shape(ws, "ws", torch.uint8, (ws.numel(),))
     _launch("experts_sort", ids, (offsets, order, pos, ws), offsets.data_ptr(), order.data_ptr(), pos.data_ptr(),
@@ -607,7 +609,7 @@ def experts_sort(offsets, order, pos, ids, ws=None) -> None:
 def _pos(pos, T):
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or pos.shape[0] != T:
         raise ValueError("pos must be T x k")
-    _shape(pos, "pos", torch.int32, tuple(pos.shape))
+    _shape(pos, "pos", torch.int32, pos.shape)
     return pos.shape[1]
 
 

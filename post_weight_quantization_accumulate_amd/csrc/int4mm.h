@@ -25,17 +25,21 @@ struct I4Args {
 enum : int { W_INT4 = 0, W_NF4_2 = 2, W_NF4_3 = 3 };
 template <int WM> struct WParts { static constexpr int n = WM == W_INT4 ? 1 : WM; };
 
-// The NF4 levels' bf16 parts, for an LDS table of 16 entries (first part in the
-// low half of .x, second in the high half, third in .y).  16 entries lie in 16
-// (.x alone) or 32 banks: lanes with different codes never meet in one.
+// The bf16 parts of the NF4 levels of a byte's two codes, the low nibble's in the
+// low half: an LDS table that turns a byte into operand dwords at one read, where
+// a table of single levels takes two reads and a byte permute per part (64 x
+// 10240 x 5120, groups of 64: 68 -> MEASURE us), though its reads meet in a bank more often.
 struct Nf4Table {
-    uint2 e[16];
+    uint2 hm[256];              // first and second parts
+    unsigned l[256];            // third parts
     __device__ void fill()
     {
-        if (threadIdx.x < 16) {
-            unsigned short h, m, l;
-            split3(kNF4[threadIdx.x], h, m, l);
-            e[threadIdx.x] = make_uint2(h | (unsigned)m << 16, l);
+        for (int i = threadIdx.x; i < 256; i += blockDim.x) {
+            unsigned short h0, m0, l0, h1, m1, l1;
+            split3(kNF4[i & 15], h0, m0, l0);
+            split3(kNF4[i >> 4], h1, m1, l1);
+            hm[i] = make_uint2(h0 | (unsigned)h1 << 16, m0 | (unsigned)m1 << 16);
+            l[i] = l0 | (unsigned)l1 << 16;
         }
     }
 };
@@ -58,11 +62,11 @@ template <int WM> __device__ inline void code_parts(unsigned w, const Nf4Table &
         u32x4 o[WM];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int c0 = (w >> (8 * t)) & 15, c1 = (w >> (8 * t + 4)) & 15;
-            const unsigned a = tab.e[c0].x, b = tab.e[c1].x;
-            o[0][t] = __builtin_amdgcn_perm(b, a, 0x05040100u);
-            o[1][t] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-            if constexpr (WM == W_NF4_3) o[2][t] = __builtin_amdgcn_perm(tab.e[c1].y, tab.e[c0].y, 0x05040100u);
+            const unsigned c = (w >> (8 * t)) & 255;
+            const uint2 v = tab.hm[c];
+            o[0][t] = v.x;
+            o[1][t] = v.y;
+            if constexpr (WM == W_NF4_3) o[2][t] = tab.l[c];
         }
 #pragma unroll
         for (int j = 0; j < WM; ++j) p[j] = __builtin_bit_cast(bf16x8, o[j]);
