@@ -28,7 +28,7 @@ template <int WM> struct WParts { static constexpr int n = WM == W_INT4 ? 1 : WM
 // The bf16 parts of the NF4 levels of a byte's two codes, the low nibble's in the
 // low half: an LDS table that turns a byte into operand dwords at one read, where
 // a table of single levels takes two reads and a byte permute per part (64 x
-// 10240 x 5120, groups of 64: 68 -> MEASURE us), though its reads meet in a bank more often.
+// 10240 x 5120, groups of 64: 68 -> 39 us), though its reads meet in a bank more often.
 struct Nf4Table {
     uint2 hm[256];              // first and second parts
     unsigned l[256];            // third parts
@@ -91,16 +91,25 @@ __device__ inline void transpose4(unsigned (&d)[4])
 // Eight consecutive elements of X from memory or LDS (16-byte pieces) as bf16 parts.
 template <typename TX> struct XParts { static constexpr int n = sizeof(TX) == 4 ? 3 : 1; };
 __device__ inline void x_parts(const __bf16 *p0, const __bf16 *, bf16x8 (&p)[1]) { p[0] = *(const bf16x8 *)p0; }
+// As split3, for eight values: an infinity stays in the first part alone; a NaN,
+// whose differences are NaN, needs no care.
 __device__ inline void x_parts(f32x4 a, f32x4 b, bf16x8 (&p)[3])
 {
     const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    unsigned d[3][8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-        unsigned short h, m, l;
-        split3(v[t], h, m, l);
-        p[0][t] = __builtin_bit_cast(__bf16, h);
-        p[1][t] = __builtin_bit_cast(__bf16, m);
-        p[2][t] = __builtin_bit_cast(__bf16, l);
+        d[0][t] = __float_as_uint(v[t]);
+        const float r = __builtin_isinf(v[t]) ? 0.0f : v[t] - __uint_as_float(d[0][t] & 0xFFFF0000u);
+        d[1][t] = __float_as_uint(r);
+        d[2][t] = __float_as_uint(r - __uint_as_float(d[1][t] & 0xFFFF0000u));
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        u32x4 o;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t] = __builtin_amdgcn_perm(d[j][2 * t + 1], d[j][2 * t], 0x07060302u);
+        p[j] = __builtin_bit_cast(bf16x8, o);
     }
 }
 // p0, p1: the two 16-byte halves (4 elements each)
