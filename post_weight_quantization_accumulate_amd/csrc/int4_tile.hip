@@ -5,15 +5,23 @@
 // of each row of X (128 k of bf16, 64 of fp32), two stages in LDS, the next
 // copied past the registers while one is multiplied.  Every wave reads the whole
 // X tile and turns only its own columns' codes into bf16, in registers: the codes
-// never go through LDS, and a code is converted once per TM rows.  Row rho of a
-// stage is 16 chunks of 16 bytes, chunk c at position c ^ (rho & 15), so 8 lanes
-// that read one chunk of 8 rows meet 8 different positions.
+// never go through LDS, and a code is converted once per TM rows.
 //
-// v_mfma_f32_16x16x32_bf16 takes 8 k from each lane; which k is free as long as X
-// and W agree.  Where a stage lies inside one group (NG = 1) lane l / 16 = q takes
-// k = (KS / 4) q + 8 h of step h, so that its codes of the whole stage are one
-// load; with NG groups per stage step h has to lie in one group and takes
-// k = 32 h + 8 q.  A group's sum is formed apart and multiplied by its scale.
+// v_mfma_f32_16x16x32_bf16 takes 8 k from each lane: step h of a stage k = 32 h +
+// 8 (l / 16) .. + 7, within one group, the group's sum formed apart and multiplied
+// by its scale.  A lane loads its row's codes 16 bytes at a time and the groups of
+// lanes exchange them (transpose4).  Row rho of a stage is 16 chunks of 16 bytes,
+// chunk c at position c ^ (rho & 15); a 16-byte LDS read is served 16 lanes at a
+// time, rows 0..3 and 12..15 of one group of 16 lanes with rows 4..11 of the next,
+// and neighbouring groups' chunks differ in their low two bits only, so the 16
+// meet different positions (a lane with 4 consecutive chunks instead: half of the
+// LDS's busy cycles were conflicts).
+//
+// 8192 x 8192 x 8192, groups of 128, bf16: 1.03 ms, 1.07 PFLOP/s, where the bf16
+// matrix cores reach 1.22 in a large library product without the codes.  A wave's
+// 128 rows amortise a code's two conversion instructions; its sums and converted
+// weights take the registers of two waves per SIMD, so conversions of one
+// workgroup run beside the matrix instructions of the other.
 #include "int4mm.h"
 
 namespace gq {
@@ -78,8 +86,8 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a, int64_t nt,
         for (int j = 0; j < PN; ++j) {
             const unsigned n = (unsigned)min(nrow + 16 * j, nlast);
             const uint8_t *c = cbase + n * (unsigned)(K / 2);
-            if constexpr (NG == 1) {
-                __builtin_memcpy(&cn[j][0], c + min((KS / 2) * b + (KS / 8) * q, K / 2 - KS / 8), KS / 8);
+            if constexpr (NH == 4) {
+                __builtin_memcpy(&cn[j][0], c + min((KS / 2) * b + 16 * q, K / 2 - 16), 16);
             } else {
 #pragma unroll
                 for (int h = 0; h < NH; ++h) __builtin_memcpy(&cn[j][h], c + min((KS / 2) * b + 16 * h + 4 * q, K / 2 - 4), 4);
@@ -103,6 +111,7 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a, int64_t nt,
         float s[PN][NG];
 #pragma unroll
         for (int j = 0; j < PN; ++j) {
+            if constexpr (NH == 4) transpose4(cn[j]);
 #pragma unroll
             for (int h = 0; h < NH; ++h) code_parts<WMODE>(cn[j][h], tab, w[j][h]);
 #pragma unroll
@@ -119,7 +128,7 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a, int64_t nt,
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 // element of the row's stage at which this lane's 8 begin, and its chunk
-                const int k0 = NG == 1 ? (KS / 4) * q + 8 * h : 32 * h + 8 * q;
+                const int k0 = 32 * h + 8 * q;
                 const int c = k0 * (int)sizeof(TX) / 16;
                 x_parts((const TX *)(xs + 16 * i * kRow + 16 * (c ^ r)), (const TX *)(xs + 16 * i * kRow + 16 * ((c + 1) ^ r)), x[h]);
             }

@@ -209,9 +209,11 @@ def test_positions_outside_the_rows_count_as_dropped(gq):
     assert dw[0, 1] == 0 and dw[1, 0] == 0 and dw[2, 0] == 0
 
 
-def test_experts_in_a_graph(gq):
+@pytest.mark.parametrize("T", [70, 1500])
+def test_experts_in_a_graph(gq, T):
+    """The one-launch sort and the one of several, with the rows' copies and sums behind it."""
     rng = np.random.default_rng(13)
-    T, k, E, D = 70, 4, 16, 136
+    k, E, D = 4, 16, 136
     ids = torch.zeros(T, k, dtype=torch.int32, device=DEV)
     x, w = torch.zeros(T, D, device=DEV), torch.zeros(T, k, device=DEV)
     off, order = torch.zeros(E + 1, dtype=torch.int32, device=DEV), torch.zeros(T * k, dtype=torch.int32, device=DEV)
