@@ -376,11 +376,41 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(F8Args a, int64_
             return;
         }
         const int r8 = 8 * (wave + NW * u);
-        if constexpr (DMA)
-            copy16_lds((r8 < TM ? xbase : wbase) + b * kStage, off[u], lbase + slot * kSlot + r8 * kStage);
-        else
-            *(u32x4 *)(lds + slot * kSlot + r8 * kStage + 16 * lane) =
-                load16((r8 < TM ? xbase : wbase) + b * kStage + off[u], K - b * kStage - (int)ch);
+        copy16_lds((r8 < TM ? xbase : wbase) + b * kStage, off[u], lbase + slot * kSlot + r8 * kStage);
+    };
+    // Without DMA (rows that do not start on 16 bytes, or K not whole blocks): the
+    // next stage's pieces come through registers, loaded before a stage is
+    // multiplied and stored after it; zero past K.
+    u32x4 held[DMA ? 1 : NC];
+    auto fetch = [&](int b) {
+        const int left = K - b * kStage - (int)ch;
+        if (b * kStage + kStage <= K) {
+#pragma unroll
+            for (int u = 0; u < NC; ++u) {
+                const int r8 = 8 * (wave + NW * u);
+                __builtin_memcpy(&held[DMA ? 0 : u], (r8 < TM ? xbase : wbase) + b * kStage + off[u], 16);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < NC; ++u) {
+                const int r8 = 8 * (wave + NW * u);
+                held[DMA ? 0 : u] = load16((r8 < TM ? xbase : wbase) + b * kStage + off[u], left);
+            }
+        }
+    };
+    auto put = [&](int slot) {
+#pragma unroll
+        for (int u = 0; u < NC; ++u)
+            *(u32x4 *)(lds + slot * kSlot + 8 * (wave + NW * u) * kStage + 16 * lane) = held[DMA ? 0 : u];
+    };
+    auto start = [&](int b, int slot) {
+        if constexpr (DMA) {
+#pragma unroll
+            for (int u = 0; u < NC; ++u) copy(b, slot, u);
+        } else {
+            fetch(b);
+        }
+        copy(b, slot, NC);
     };
 
     const int r = lane & 15, q = lane >> 4;
@@ -420,9 +450,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(F8Args a, int64_
     // (64 experts, 4000 rows: 136 against 156 us).
     f32x4 part[2][PN];
     float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int u = 0; u <= NC; ++u) copy(0, 0, u);
+    start(0, 0);
+    if constexpr (!DMA) put(0);
     if constexpr (PINNED) {
+        static_assert(DMA || !PINNED, "the pinned order copies past the registers");
         constexpr int CPS = (NC + 1 + PM - 1) / PM;      // copies per step
 #pragma unroll
         for (int j = 0; j < PN; ++j) part[1][j] = f32x4{};
@@ -467,10 +498,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(F8Args a, int64_
         for (int b = 0; b < kb; ++b) {
             const int slot = b & 1;
             publish();
-            if (b + 1 < kb) {
-#pragma unroll
-                for (int u = 0; u <= NC; ++u) copy(b + 1, slot ^ 1, u);
-            }
+            if (b + 1 < kb) start(b + 1, slot ^ 1);
             const uint8_t *xs_ = lds + slot * kSlot + 16 * PM * wm * kStage;
             const uint8_t *ws_ = lds + slot * kSlot + (TM + 16 * PN * wn) * kStage;
             const float s_w = sw[b];
@@ -487,6 +515,9 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tile_kernel(F8Args a, int64_
                 for (int j = 0; j < PN; ++j)
 #pragma unroll
                     for (int t = 0; t < 4; ++t) acc[i][j][t] = fmaf(s[0], part[0][j][t], acc[i][j][t]);
+            }
+            if constexpr (!DMA) {
+                if (b + 1 < kb) put(slot ^ 1);
             }
         }
     }

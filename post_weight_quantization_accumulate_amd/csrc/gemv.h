@@ -22,8 +22,8 @@ struct GemvArgs {
 
 // Rows per tile above which the matrix cores win.
 constexpr int kGemvMaxRows = 2;
-// True if the kernel takes these sizes: rows of whole 16-byte pieces of 32 codes
-// (int4) or twice that (fp8), at most 16 waves to a row.
+// True if the kernel takes these sizes: at least one piece of 32 codes to a row
+// (int4: whole pieces), scales no finer than that, at most 16 waves to a row.
 bool gemv_ok(const GemvArgs &a, int kind, int rows);
 hipError_t launch_gemv(const GemvArgs &a, int kind, int rows, hipStream_t s);
 

@@ -115,13 +115,16 @@ __global__ __launch_bounds__(MAXT) void gemv_kernel(GemvArgs a)
     if (!row_tile(a.offsets, (int)a.E, a.M, MR, grid_row(), rt)) return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), WR = (int)(blockDim.x >> 6);
-    const int n0 = blockIdx.x * COLS, segs = a.K / SEG;
+    const int n0 = blockIdx.x * COLS, segs = (a.K + SEG - 1) / SEG;
     const int sg = min(wave * 64 + lane, segs - 1);
+    // a last segment that is not whole (e4m3 only) ends with the row; the x of what
+    // belongs to the lane before it are zero
+    const int k0 = min(sg * SEG, a.K - SEG), over = sg * SEG - k0;
     const bool in = wave * 64 + lane < segs;                         // lanes past the row add zeros
     const int64_t rowb = KIND == GEMV_FP8 ? a.K : a.K / 2;
     const int nsc = KIND == GEMV_FP8 ? (a.K + 127) / 128 : a.K / a.G;      // scales per row
     const int lg = __builtin_ctz(a.G);
-    const uint8_t *cb = a.codes + rt.e * a.N * rowb + (int64_t)sg * CB;
+    const uint8_t *cb = a.codes + rt.e * a.N * rowb + (int64_t)k0 * CB / SEG;
     const float *sb = a.scales + rt.e * (KIND == GEMV_FP8 ? (a.N + 127) / 128 : a.N) * (int64_t)nsc + ((sg * SEG) >> lg);
     u32x4 c[COLS][NL];
     float sc[COLS];
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(MAXT) void gemv_kernel(GemvArgs a)
     for (int b = 0; b < COLS; ++b) {
         const int n = min(n0 + b, a.N - 1);
 #pragma unroll
-        for (int l = 0; l < NL; ++l) c[b][l] = *(const u32x4 *)(cb + n * rowb + 16 * l);
+        for (int l = 0; l < NL; ++l) __builtin_memcpy(&c[b][l], cb + n * rowb + 16 * l, 16);
         sc[b] = sb[(KIND == GEMV_FP8 ? n / 128 : n) * (int64_t)nsc];
     }
     float x[MR][SEG];
@@ -138,7 +141,7 @@ __global__ __launch_bounds__(MAXT) void gemv_kernel(GemvArgs a)
         const int64_t row = min(rt.r0 + m, rt.r1 - 1);
         if constexpr (KIND == GEMV_FP8) {
             u32x4 v[2];
-            __builtin_memcpy(v, (const uint8_t *)a.X + row * a.K + sg * SEG, 32);
+            __builtin_memcpy(v, (const uint8_t *)a.X + row * a.K + k0, 32);
             const float s = a.xs[row * nsc + (sg * SEG >> 7)];
             typedef float f32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -151,7 +154,7 @@ __global__ __launch_bounds__(MAXT) void gemv_kernel(GemvArgs a)
             load_x32((const TX *)a.X + row * a.ldx + sg * SEG, x[m]);
         }
 #pragma unroll
-        for (int t = 0; t < SEG; ++t) x[m][t] = in ? x[m][t] : 0.0f;
+        for (int t = 0; t < SEG; ++t) x[m][t] = in && (KIND != GEMV_FP8 || t >= over) ? x[m][t] : 0.0f;
     }
 #pragma unroll
     for (int b0 = 0; b0 < COLS; b0 += 4) {
@@ -191,6 +194,9 @@ __global__ __launch_bounds__(MAXT) void gemv_kernel(GemvArgs a)
     }
 }
 
+// Waves to a row of the pack.
+constexpr int row_waves(int K) { return ((K + SEG - 1) / SEG + 63) / 64; }
+
 // Waves of a workgroup that leave each the registers its x need.
 constexpr int max_waves(int mr) { return mr == 1 ? 16 : 10; }
 
@@ -201,7 +207,7 @@ template <int KIND, typename TX, int MR, int COLS> hipError_t launch_cols(const 
 {
     hipLaunchKernelGGL((gemv_kernel<KIND, TX, MR, COLS, 64 * max_waves(MR)>),
                        tile_grid((a.N + COLS - 1) / COLS, row_tiles(a.offsets != nullptr, a.E, a.M, MR)),
-                       dim3(64 * ((a.K / SEG + 63) / 64)), 0, s, a);
+                       dim3(64 * row_waves(a.K)), 0, s, a);
     return hipGetLastError();
 }
 template <int KIND, typename TX, int MR> hipError_t launch_rows(const GemvArgs &a, hipStream_t s)
@@ -219,8 +225,8 @@ template <int KIND, typename TX> hipError_t by_rows(const GemvArgs &a, int rows,
 
 bool gemv_ok(const GemvArgs &a, int kind, int rows)
 {
-    return rows <= kGemvMaxRows && a.K % SEG == 0 && a.G >= SEG && (a.K / SEG + 63) / 64 <= max_waves(rows) &&
-           ((uintptr_t)a.codes & 15) == 0;
+    return rows <= kGemvMaxRows && a.G >= SEG && row_waves(a.K) <= max_waves(rows) &&
+           (kind == GEMV_FP8 ? a.K >= SEG : a.K % SEG == 0);
 }
 
 hipError_t launch_gemv(const GemvArgs &a, int kind, int rows, hipStream_t s)

@@ -267,7 +267,8 @@ def _deq8(codes, scales, br):
                                    (64, 300, 1024), (65, 257, 129), (130, 256, 640), (300, 384, 512), (257, 515, 2176),
                                    (513, 260, 136), (2, 1024, 5120), (600, 512, 384), (40, 1000, 4100),
                                    (33, 130, 1008), (5, 64, 144), (17, 40, 16), (1, 30, 17408), (1, 20, 33280), (2, 24, 20608),
-                                   (1, 40, 96), (3, 50, 640), (4200, 260, 256), (700, 2050, 128)])
+                                   (1, 40, 96), (1, 33, 33), (2, 70, 5001), (1, 4100, 1000), (1, 9, 31), (2, 20, 161),
+                                   (3, 50, 640), (4200, 260, 256), (700, 2050, 128)])
 def test_fp8_matmul(gq, M, N, K, yd):
     rng = np.random.default_rng(M + N + K)
     xq, xs = _pack8(gq, _x(rng, M, K, torch.float32), 1)
@@ -324,13 +325,14 @@ def test_fp8_matmul_experts(gq, counts, M, N, K, yd):
     assert (y[off[-1]:] == 7.0).all()
 
 
+@pytest.mark.parametrize("K", [256, 250])
 @pytest.mark.parametrize("M", [2, 20, 300])
-def test_fp8_matmul_nan_stays_in_its_row(gq, M):
+def test_fp8_matmul_nan_stays_in_its_row(gq, M, K):
     rng = np.random.default_rng(4)
-    x = _x(rng, M, 256, torch.float32)
+    x = _x(rng, M, K, torch.float32)
     x[1, 200] = float("nan")
     xq, xs = _pack8(gq, x, 1)
-    wq, ws = _pack8(gq, _x(rng, 256, 256, torch.float32), 128)
+    wq, ws = _pack8(gq, _x(rng, 256, K, torch.float32), 128)
     y = torch.zeros(M, 256, device=DEV)
     gq.fp8_matmul(y, xq, xs, wq, ws)
     assert torch.isnan(y[1]).all() and torch.isfinite(y[0]).all() and torch.isfinite(y[2:]).all()
