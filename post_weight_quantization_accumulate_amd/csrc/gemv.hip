@@ -200,9 +200,6 @@ constexpr int row_waves(int K) { return ((K + SEG - 1) / SEG + 63) / 64; }
 // Waves of a workgroup that leave each the registers its x need.
 constexpr int max_waves(int mr) { return mr == 1 ? 16 : 10; }
 
-// Eight columns share each x; with fewer than two workgroups per CU of them
-// (N < 4096), four (1 x 1024 x 5120: 3.5 against 4.0 us; 1 x 10240 x 5120: 10.2
-// against 9.0).
 template <int KIND, typename TX, int MR, int COLS> hipError_t launch_cols(const GemvArgs &a, hipStream_t s)
 {
     hipLaunchKernelGGL((gemv_kernel<KIND, TX, MR, COLS, 64 * max_waves(MR)>),
@@ -210,9 +207,18 @@ template <int KIND, typename TX, int MR, int COLS> hipError_t launch_cols(const 
                        dim3(64 * row_waves(a.K)), 0, s, a);
     return hipGetLastError();
 }
+// Eight columns share each x and are the rule.  Four leave fewer CUs without work
+// where there are fewer than two workgroups to a CU (1 x 1024 x 5120: 3.3 against
+// 4.0 us), or where those of eight would fill their last round badly (1 x 5120 x
+// 17408 int4, 640 workgroups of which 512 run at a time: 14.9 against 19.4 us; 1 x
+// 8192 x 28672, four full rounds: 38.9 against 33.6 us).
 template <int KIND, typename TX, int MR> hipError_t launch_rows(const GemvArgs &a, hipStream_t s)
 {
-    return a.N >= 4096 ? launch_cols<KIND, TX, MR, 8>(a, s) : launch_cols<KIND, TX, MR, 4>(a, s);
+    constexpr int kWaves = MR == 2 ? 12 : KIND == GEMV_INT4 ? 20 : 16;      // to a CU, by the registers
+    const int64_t wgs = (a.N + 7) / 8 * row_tiles(a.offsets != nullptr, a.E, a.M, MR);
+    const int64_t slots = 256 * (row_waves(a.K) < kWaves ? kWaves / row_waves(a.K) : 1);
+    const bool badly = wgs > slots && 4 * wgs < 3 * slots * ((wgs + slots - 1) / slots);
+    return wgs < 512 || badly ? launch_cols<KIND, TX, MR, 4>(a, s) : launch_cols<KIND, TX, MR, 8>(a, s);
 }
 
 template <int KIND, typename TX> hipError_t by_rows(const GemvArgs &a, int rows, hipStream_t s)
