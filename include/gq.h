@@ -30,7 +30,8 @@
  *   - Calls return a gq_status.  GQ_OK is 0; the detail of any other status is
  *     in gq_last_error() (thread-local, valid until the next call on the same
  *     host thread).  On an error the outputs are undefined.
- *   - hessian_* calls (and the pack products and expert rows below) are asynchronous: they validate arguments, enqueue kernels
+ *   - hessian_* calls (and the pack products and expert rows at the end of this
+ *     file) are asynchronous: they validate arguments, enqueue kernels
  *     and return; they report argument and launch errors only.  psd_project,
  *     gptq_factor, gptq_sweep and gptq_quantize synchronise their stream before
  *     returning, to report data-dependent status (and qerr).
@@ -413,7 +414,8 @@ int rtn_quantize_noalloc(uint8_t *codes, float *scales, double *qerr_out, const 
  *     workspace;
  *   - outputs must not overlap inputs; the stream belongs to the current device;
  *   - the same inputs give the same bits: no sum depends on timing;
- *   - NaN and infinity are not searched for: they spread as in the formula.
+ *   - NaN and infinity in X are not searched for: they spread as in the formula;
+ *   - products take N up to 2^24, K up to 2^22 and X's rows up to 2^22 apart.
  * An expert's rows are offsets[e] .. offsets[e + 1] - 1 (int32, device, E + 1
  * entries, as experts_sort writes them) of a matrix of M rows; rows outside
  * offsets[0] .. offsets[E] - 1 of the output are left as they were.  Entries

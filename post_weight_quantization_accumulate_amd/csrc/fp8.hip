@@ -211,11 +211,11 @@ __device__ inline int chunk_pos(int c, int row) { return c ^ ((row >> 1) & 7); }
 // each, one block of 128 k at a time, through rings of their own in LDS (see
 // ring), and add their sums in wave order.  A copy is 8 rows of 128 bytes, whole
 // cache lines.
-template <typename TY, int MT, int NT, int W, int D>
+template <typename TY, int MT, int NT, int W>
 __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(F8Args a)
 {
     constexpr int C = 2 * (MT + NT), XB = 2048 * MT, SLOT = XB + 2048 * NT + 256 * MT;    // X, W, X's scales
-    static_assert(D * SLOT >= MT * NT * 1024, "the sums reuse the ring's space");
+    static_assert(2 * SLOT >= MT * NT * 1024, "the sums reuse the ring's space");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     RowTile rt;
     if (!row_tile(a.offsets, (int)a.E, a.M, 16 * MT, grid_row(), rt)) return;
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(F8Args a)
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) so[i] = 4u * (unsigned)min(16 * i + r, mrows - 1) * (unsigned)kb;
-    uint8_t *mine = lds + wave * D * SLOT;
+    uint8_t *mine = lds + wave * 2 * SLOT;
     const unsigned mo = lds_offset(mine);
     constexpr int LOADS = C + MT;
     auto issue = [&](int b, int slot) {
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(F8Args a)
         }
     };
     const int per = (kb + W - 1) / W, b0 = wave * per;
-    ring<D, LOADS>(b0, min(b0 + per, kb), issue, use);
+    ring<LOADS>(b0, min(b0 + per, kb), issue, use);
     __syncthreads();                                     // every wave is past its ring
     float *red = (float *)lds;
     // acc[i][j][t]: column 16 j + 4 q + t of row 16 i + r
@@ -307,11 +307,11 @@ __global__ __launch_bounds__(64 * W) void fp8_skinny_kernel(F8Args a)
     }
 }
 
-template <typename TY, int MT, int NT, int W, int D> hipError_t launch_skinny(const F8Args &a, hipStream_t s)
+template <typename TY, int MT, int NT, int W> hipError_t launch_skinny(const F8Args &a, hipStream_t s)
 {
-    constexpr size_t lds = (size_t)W * D * (2048 * (MT + NT) + 256 * MT);
+    constexpr size_t lds = (size_t)W * 2 * (2048 * (MT + NT) + 256 * MT);
     static_assert(lds <= 160 * 1024, "LDS");
-    constexpr auto kernel = fp8_skinny_kernel<TY, MT, NT, W, D>;
+    constexpr auto kernel = fp8_skinny_kernel<TY, MT, NT, W>;
     const hipError_t e = allow_lds<kernel>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, tile_grid((a.N + 16 * NT - 1) / (16 * NT), row_tiles(a.offsets != nullptr, a.E, a.M, 16 * MT)),
@@ -325,9 +325,10 @@ template <typename TY, int MT, int NT, int W, int D> hipError_t launch_skinny(co
 // LDS: while one is multiplied the next is copied into the other.
 //
 // v_mfma_f32_16x16x128_f8f6f4 covers exactly one scale block: lane l feeds 32
-// codes of row l % 16 of each operand, and the weights go first, so a lane's 4 results are columns 4 (l / 16) + 0..3 of row l % 16 of Y
-// and share one scale xs[m] ws[n / 128].  The scaled sums must be in VGPRs (the
-// matrix cores alone reach the AGPRs), so a wave holds at most 128 of them.
+// codes of row l % 16 of each operand, and the weights go first, so a lane's 4
+// results are columns 4 (l / 16) + 0..3 of row l % 16 of Y and share one scale
+// xs[m] ws[n / 128].  The scaled sums must be in VGPRs (the matrix cores alone
+// reach the AGPRs), so a wave holds at most 128 of them.
 // With F8 false (fp32 outputs) the codes are turned into bf16 instead.
 constexpr int kStage = 128;
 
@@ -583,9 +584,9 @@ template <typename TY> hipError_t launch_fp8(F8Args a, hipStream_t s)
     const double mid = tmid <= 512 ? 42 : 54 * std::max(1.0, (double)tmid / 768);
     const int best = small[2] < small[0] ? (small[2] < small[1] ? 2 : 1) : (small[1] < small[0] ? 1 : 0);
     if (dma && small[best] < mid) {
-        if (best == 0) return launch_skinny<TY, 1, 1, 4, 2>(a, s);
-        if (best == 1) return launch_skinny<TY, 1, 2, 8, 2>(a, s);
-        return launch_skinny<TY, 2, 2, 4, 2>(a, s);
+        if (best == 0) return launch_skinny<TY, 1, 1, 4>(a, s);
+        if (best == 1) return launch_skinny<TY, 1, 2, 8>(a, s);
+        return launch_skinny<TY, 2, 2, 4>(a, s);
     }
     // the large tile's sums leave no registers for codes turned into bf16, or for
     // copies through registers

@@ -5,12 +5,13 @@
 // as fp32, and for each column n of Y (row n of the pack) it loads its 16 bytes of
 // int4 codes (32 of e4m3), neighbouring lanes neighbouring bytes, so every load of
 // a wave is one contiguous run.  A workgroup is the waves of one row of the pack
-// and takes COLS columns, all their loads issued at once.  All arithmetic is fp32 (codes, NF4 levels and e4m3
-// values are exact in it); a lane's 32 products lie within one group and are
-// scaled once.  The four sums of a wave are reduced together: two of them change
-// halves (then quarters) with one swap, so it takes 10 instructions, not 24.
+// and takes COLS columns, all their loads issued at once.  All arithmetic is fp32
+// (codes, NF4 levels and e4m3 values are exact in it); a lane's 32 products lie
+// within one group and are scaled once.  The four sums of a wave are reduced
+// together: two of them change halves (then quarters) with one swap, so it takes
+// 10 instructions, not 24.
 // The matrix cores would need each lane's loads 16 rows apart and x loaded again
-// for every 16 columns.  Bound by memory: 1 x 5120 x 17408 e4m3 takes 20 us (4.4
+// for every 16 columns.  Bound by memory: 1 x 5120 x 17408 e4m3 takes 21 us (4.2
 // TB/s, a large copy reaches 5.2), 1 x 10240 x 5120 int4 8.7 us (3.2 TB/s; the
 // arithmetic, 2.4 instructions per code, takes about 3 of them).
 #include "gemv.h"

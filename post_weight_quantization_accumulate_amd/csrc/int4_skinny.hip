@@ -9,7 +9,8 @@
 // through LDS in whole lines instead (16 x 5120 x 10240: 20.7 -> 13.4 us).  Codes
 // and scales take the same way, so that the waits are the ring's own: the
 // compiler's, which does not know of the copies, would wait for those too.  The
-// ring is the wave's own part of LDS, with no barrier.
+// ring is the wave's own part of LDS, with no barrier; a deeper one leaves fewer
+// workgroups to a CU (16 x 10240 x 5120: 13.4 / 14.0 / 17.7 us with 2, 3, 4 slots).
 #include "int4mm.h"
 
 namespace gq {
@@ -19,18 +20,18 @@ constexpr int KU = 128, NH = KU / 32;
 
 // XC: copies of X per unit, 1 KiB each; rows past them (there are none) hold
 // whatever was in LDS, in rows of Y that are not stored.
-template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC, int D>
+template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC>
 __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
 {
     constexpr int PX = XParts<TX>::n, PW = WParts<WMODE>::n;
     constexpr int ROWB = KU * (int)sizeof(TX), RC = 1024 / ROWB;            // bytes per row, rows per copy
     constexpr int XB = 16 * MT * ROWB, SLOT = XB + NT * (1024 + 256);               // X, codes, scales
     static_assert(XC * RC <= 16 * MT, "copies");
-    static_assert(D * SLOT >= MT * NT * 1024, "the sums reuse the ring's space");
+    static_assert(2 * SLOT >= MT * NT * 1024, "the sums reuse the ring's space");
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     __shared__ Nf4Table tab;
     if constexpr (WMODE != W_INT4) {
-        tab.fill();
+        tab.fill<PW>();
         __syncthreads();
     }
     RowTile rt;
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     // copy i: rows RC i .. of the unit; the 16-byte chunk c of row rho lies at
     // position c ^ (rho & 15), so 8 lanes that read one chunk of 8 rows meet 8
     // different positions
-    uint8_t *xl = lds + wave * D * SLOT;
+    uint8_t *xl = lds + wave * 2 * SLOT;
     const unsigned xlo = lds_offset(xl);
     unsigned xo[XC], xc[XC];
 #pragma unroll
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     };
     const int units = (K + KU - 1) / KU, per = (units + W - 1) / W;
     const int u0 = wave * per, u1 = min(u0 + per, units);
-    ring<D, LOADS>(u0, u1, issue, multiply);
+    ring<LOADS>(u0, u1, issue, multiply);
     __syncthreads();                                     // every wave is past its X
     float *red = (float *)lds;                           // [W][MT * NT * 256]
 #pragma unroll
@@ -153,11 +154,11 @@ __global__ __launch_bounds__(64 * W) void int4_skinny_kernel(I4Args a)
     }
 }
 
-template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC, int D> hipError_t launch(const I4Args &a, hipStream_t s)
+template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC> hipError_t launch(const I4Args &a, hipStream_t s)
 {
-    constexpr size_t lds = (size_t)W * D * (16 * MT * KU * sizeof(TX) + NT * (1024 + 256));
+    constexpr size_t lds = (size_t)W * 2 * (16 * MT * KU * sizeof(TX) + NT * (1024 + 256));
     static_assert(lds + sizeof(Nf4Table) <= 160 * 1024, "LDS");
-    constexpr auto kernel = int4_skinny_kernel<TX, WMODE, NG, MT, NT, W, XC, D>;
+    constexpr auto kernel = int4_skinny_kernel<TX, WMODE, NG, MT, NT, W, XC>;
     const hipError_t e = allow_lds<kernel>(lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, tile_grid((a.N + 16 * NT - 1) / (16 * NT), row_tiles(a.offsets != nullptr, a.E, a.M, 16 * MT)),
@@ -170,10 +171,9 @@ template <typename TX, int WMODE, int NG, int MT, int NT, int W, int XC, int D> 
 template <typename TX, int WMODE, int NG> hipError_t by_rows(const I4Args &a, int shape, hipStream_t s)
 {
     constexpr int C16 = 16 * KU * (int)sizeof(TX) / 1024;        // copies for 16 rows
-    constexpr int D = 2;        // deeper rings leave fewer workgroups to a CU: 13.4 / 14.0 / 17.7 us for 2, 3, 4 at 16 x 10240 x 5120
-    if (shape == 2) return launch<TX, WMODE, NG, 2, 2, 4, 2 * C16, D>(a, s);
-    if (a.M <= 4) return shape ? launch<TX, WMODE, NG, 1, 2, 4, C16 / 4, D>(a, s) : launch<TX, WMODE, NG, 1, 1, 4, C16 / 4, D>(a, s);
-    return shape ? launch<TX, WMODE, NG, 1, 2, 4, C16, D>(a, s) : launch<TX, WMODE, NG, 1, 1, 4, C16, D>(a, s);
+    if (shape == 2) return launch<TX, WMODE, NG, 2, 2, 4, 2 * C16>(a, s);
+    if (a.M <= 4) return shape ? launch<TX, WMODE, NG, 1, 2, 4, C16 / 4>(a, s) : launch<TX, WMODE, NG, 1, 1, 4, C16 / 4>(a, s);
+    return shape ? launch<TX, WMODE, NG, 1, 2, 4, C16>(a, s) : launch<TX, WMODE, NG, 1, 1, 4, C16>(a, s);
 }
 
 template <typename TX, int WMODE> hipError_t by_group(const I4Args &a, int shape, hipStream_t s)

@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(I4Args a, int64_t nt,
     __shared__ Nf4Table tab;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    if constexpr (WMODE != W_INT4) tab.fill();
+    if constexpr (WMODE != W_INT4) tab.fill<PW>();
     int64_t ti, tj;
     grouped_tile(blockIdx.x, nt, mt, ti, tj);
     RowTile rt;

@@ -25,6 +25,21 @@ struct I4Args {
 enum : int { W_INT4 = 0, W_NF4_2 = 2, W_NF4_3 = 3 };
 template <int WM> struct WParts { static constexpr int n = WM == W_INT4 ? 1 : WM; };
 
+// fp32 as N bf16 parts of its sign, 8 leading bits of what is left each, by
+// truncation: three parts are exact.  No part but the last takes all that is left,
+// so none is 0 unless the weight is: an infinite x then gives an infinity, not
+// infinity times 0.
+template <int N> __device__ inline void weight_parts(float v, unsigned short (&p)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        unsigned b = __float_as_uint(v) & 0xFFFF0000u;
+        if (j + 1 < N && v != 0.0f && __uint_as_float(b) == v) b -= 0x10000u;
+        p[j] = (unsigned short)(b >> 16);
+        v -= __uint_as_float(b);
+    }
+}
+
 // The bf16 parts of the NF4 levels of a byte's two codes, the low nibble's in the
 // low half: an LDS table that turns a byte into operand dwords at one read, where
 // a table of single levels takes two reads and a byte permute per part (64 x
@@ -32,14 +47,14 @@ template <int WM> struct WParts { static constexpr int n = WM == W_INT4 ? 1 : WM
 struct Nf4Table {
     uint2 hm[256];              // first and second parts
     unsigned l[256];            // third parts
-    __device__ void fill()
+    template <int N> __device__ void fill()
     {
         for (int i = threadIdx.x; i < 256; i += blockDim.x) {
-            unsigned short h0, m0, l0, h1, m1, l1;
-            split3(kNF4[i & 15], h0, m0, l0);
-            split3(kNF4[i >> 4], h1, m1, l1);
-            hm[i] = make_uint2(h0 | (unsigned)h1 << 16, m0 | (unsigned)m1 << 16);
-            l[i] = l0 | (unsigned)l1 << 16;
+            unsigned short p[N], o[N];
+            weight_parts(kNF4[i & 15], p);
+            weight_parts(kNF4[i >> 4], o);
+            hm[i] = make_uint2(p[0] | (unsigned)o[0] << 16, p[1] | (unsigned)o[1] << 16);
+            if constexpr (N == 3) l[i] = p[2] | (unsigned)o[2] << 16;
         }
     }
 };
@@ -91,8 +106,8 @@ __device__ inline void transpose4(unsigned (&d)[4])
 // Eight consecutive elements of X from memory or LDS (16-byte pieces) as bf16 parts.
 template <typename TX> struct XParts { static constexpr int n = sizeof(TX) == 4 ? 3 : 1; };
 __device__ inline void x_parts(const __bf16 *p0, const __bf16 *, bf16x8 (&p)[1]) { p[0] = *(const bf16x8 *)p0; }
-// As split3, for eight values: an infinity stays in the first part alone; a NaN,
-// whose differences are NaN, needs no care.
+// fp32 as three parts of 8 leading bits by truncation, exactly: an infinity stays
+// in the first part alone; a NaN, whose differences are NaN, needs no care.
 __device__ inline void x_parts(f32x4 a, f32x4 b, bf16x8 (&p)[3])
 {
     const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};

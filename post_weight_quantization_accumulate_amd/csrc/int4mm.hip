@@ -76,7 +76,7 @@ template <typename TX, bool NF4, bool K8> __global__ __launch_bounds__(64 * kWav
             const int k = k0 + 8 * q + t;
             const float s = k < a.K ? sc[k >> lg] : 0.0f;
             unsigned short p[3];
-            split3(lut[(cw >> (4 * t)) & 15] * s, p[0], p[1], p[2]);
+            weight_parts(lut[(cw >> (4 * t)) & 15] * s, p);
 #pragma unroll
             for (int j = 0; j < 3; ++j) wp[j][t] = __builtin_bit_cast(__bf16, p[j]);
         }

@@ -105,24 +105,6 @@ inline dim3 tile_grid(int64_t nt, int64_t mt)
 }
 __device__ inline int64_t grid_row() { return (int64_t)blockIdx.z * kGridRows + blockIdx.y; }
 
-// fp32 as a sum of three bf16 values, 8 leading bits each, by truncation: the
-// sum is exact for every finite value whose last part is not below bf16's
-// smallest (2^-133).  Infinity and NaN go into the first part alone, so that
-// they meet the other operand as they would unsplit.
-__device__ inline void split3(float v, unsigned short &h, unsigned short &m, unsigned short &l)
-{
-    const unsigned b = __float_as_uint(v);
-    const bool special = (b & 0x7F800000u) == 0x7F800000u;
-    unsigned hb = b & 0xFFFF0000u;
-    if (special && (b & 0x007FFFFFu)) hb |= 0x00400000u;     // a NaN stays one
-    const float r = special ? 0.0f : v - __uint_as_float(hb);
-    const unsigned mb = __float_as_uint(r) & 0xFFFF0000u;
-    const float q = r - __uint_as_float(mb);
-    h = (unsigned short)(hb >> 16);
-    m = (unsigned short)(mb >> 16);
-    l = (unsigned short)(__float_as_uint(q) >> 16);
-}
-
 // Workgroup `w` of nt x mt tiles: each XCD gets a contiguous run of tiles (see
 // xcd_order), which walk the grid in groups of kGroupRows row tiles, so that the
 // tiles that run together on one XCD share their operands in its L2.
@@ -163,34 +145,24 @@ __device__ inline void wait_lds()
     asm volatile("" ::: "memory");
 }
 
-// Runs the units u0 .. u1 - 1 of a wave through a ring of D slots of its own part
-// of LDS: issue(u, slot) starts the LOADS copies of a unit, use(u, slot) consumes
-// it.  D - 1 units are under way while one is used.  Only copies (which the
-// compiler does not know of) load from memory in here, so that the waits are
-// these alone.
-template <int D, int LOADS, typename Issue, typename Use> __device__ inline void ring(int u0, int u1, Issue issue, Use use)
+// Runs the units u0 .. u1 - 1 of a wave through two slots of its own part of LDS:
+// issue(u, slot) starts the LOADS copies of a unit, use(u, slot) consumes it while
+// the next unit's are under way.  Only copies (which the compiler does not know
+// of) load from memory in here, so that the waits are these alone.
+template <int LOADS, typename Issue, typename Use> __device__ inline void ring(int u0, int u1, Issue issue, Use use)
 {
-    static_assert(D >= 2 && D <= 4 && (D - 1) * LOADS < 64, "vmcnt");
-    int in = 0;                                      // slot of the next unit to issue
-    int u = u0;
-    for (; u < u0 + D - 1 && u < u1; ++u) issue(u, in++);
-    int out = 0;
-    for (int v = u0; v < u1; ++v) {
-        if (u < u1) {
+    if (u0 < u1) issue(u0, 0);
+    int slot = 0;
+    for (int u = u0; u < u1; ++u) {
+        if (u + 1 < u1) {
             wait_lds();
-            issue(u, in);
-            ++u;
-            in = in + 1 == D ? 0 : in + 1;
-            wait_copies<(D - 1) * LOADS>();
+            issue(u + 1, slot ^ 1);
+            wait_copies<LOADS>();
         } else {
-            // the last units: fewer are under way
-            const int left = u1 - 1 - v;
-            if (D > 3 && left >= 2) wait_copies<2 * LOADS>();
-            else if (D > 2 && left >= 1) wait_copies<LOADS>();
-            else wait_copies<0>();
+            wait_copies<0>();
         }
-        use(v, out);
-        out = out + 1 == D ? 0 : out + 1;
+        use(u, slot);
+        slot ^= 1;
     }
 }
 

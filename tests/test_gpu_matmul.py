@@ -143,6 +143,25 @@ def test_int4_matmul_special_values(gq, xd, M):
         _check(y, x64 @ w.T, np.abs(x64) @ np.abs(w).T, K, big)
 
 
+@pytest.mark.parametrize("xd,yd", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("nf4", [False, True])
+@pytest.mark.parametrize("M,K,G", [(1, 256, 64), (2, 256, 128), (20, 256, 128), (20, 224, 32), (300, 256, 64), (300, 320, 64), (40, 256, 16)])
+def test_int4_matmul_infinity_times_every_code(gq, M, K, G, nf4, xd, yd):
+    """An infinite x gives each column the infinity of its weight's sign (NaN for a weight of 0)."""
+    N = 64
+    rng = np.random.default_rng(M + K)
+    x = _x(rng, M, K, DT[xd])
+    x[0, 5] = float("inf")
+    codes, scales = _pack4(rng, N, K, G)
+    codes[:, 2] = ((np.arange(N) % 16) << 4) | 3             # column 5: every code
+    y = torch.empty((M, N), dtype=DT[yd], device=DEV)
+    gq.int4_matmul(y, x.to(DEV), torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), G, gq.GQ_NF4 if nf4 else 0)
+    w = _deq4(gq, codes, scales, G, nf4)[:, 5]
+    want = np.where(w == 0, np.nan, np.sign(w) * np.inf)
+    np.testing.assert_array_equal(y[0].double().cpu().numpy(), want)
+    assert torch.isfinite(y[1:]).all()
+
+
 @pytest.mark.parametrize("counts,M", [([0, 5, 0, 17, 1, 40], 63), ([3], 3), ([0, 0, 0], 4), ([16] * 8, 128),
                                       ([1] * 70, 70), ([300, 0, 2, 257], 560), ([0, 700], 700), ([513, 31, 64], 608)])
 @pytest.mark.parametrize("nf4,xd,G", [(False, "bf16", 128), (True, "fp32", 64), (False, "fp32", 32), (True, "bf16", 128),
